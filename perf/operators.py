@@ -10,7 +10,7 @@ written in elementary torch operations in 32 bits; with `own` true it is the lib
                    projections recomputed from x (OwqGated.backward)
   clip             the global 2-norm of many gradient tensors and the tensors scaled by
                    min(1, max_norm / (norm + 1e-6)), written to an optimiser's buffers
-                   (clip_grads)
+                   (OwqGradClip)
 
 An OWQ weight is W[i, j] = fp16_rn(s (q - z)) with (s, z) per row and group of input columns,
 except in the layer's weak columns, which hold fp16 values.
@@ -159,8 +159,12 @@ def prepare(case, seed):
     if case["op"] == "clip":
         flat, at, max_norm = _draw_grads(case, seed)
         out = torch.zeros_like(flat)
-        return {"case": case, "grads": [flat[o:o + n] for o, n in at], "outs": [out[o:o + n] for o, n in at],
-                "out": out, "max_norm": max_norm}
+        state = {"case": case, "grads": [flat[o:o + n] for o, n in at], "outs": [out[o:o + n] for o, n in at],
+                 "out": out, "max_norm": max_norm}
+        if own:   # the list of tensors that a training loop makes once
+            import weight_only_mixed_owq_b200 as owq
+            state["clip"] = owq.OwqGradClip(state["grads"], state["outs"])
+        return state
     d = _draw_block(case, seed)
     state = {"case": case, "x": d["x"], "dh": d.get("dh")}
     if own:
@@ -190,9 +194,7 @@ def _act(g, act):
 def _run_own(state):
     case = state["case"]
     if case["op"] == "clip":
-        import weight_only_mixed_owq_b200 as owq
-        norm = owq.clip_grads(state["grads"], state["max_norm"], outs=state["outs"])
-        return {"norm": norm, "grads": state["out"]}
+        return {"norm": state["clip"](state["max_norm"]), "grads": state["out"]}
     block = state["block"]
     if case["op"] == "forward":
         return block.gemv(state["x"]) if case["M"] <= 16 else block.gemm(state["x"])
