@@ -9,6 +9,7 @@
 // in place of their zero-filled codes.  Both accumulate in fp32.
 #include "owq_internal.cuh"
 #include "owq_format.cuh"
+#include "owq_mma.cuh"
 #include "owq_sm100.cuh"
 
 namespace owq {
@@ -70,23 +71,6 @@ k_weak_grad(const __half* __restrict__ x, const __half* __restrict__ dy,
 // split order, so repeated calls give the same bits.
 constexpr int kWmRows = 64, kWmCols = 32, kWmTok = 32, kWmThreads = 128, kWmStages = 4;
 constexpr int kWmDyLd = kWmRows + 8, kWmXLd = kWmCols + 8;   // padded row strides (halves)
-
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool valid) {
-  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-  const int n = valid ? 16 : 0;   // 0: the 16 bytes are filled with zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(d), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], const void* p) {
-  const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
-}
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-               "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 
 // xw[m][t] = x[m][idx[t]] for t < k, 0 for k <= t < kp
 __global__ void k_wg_gather(const __half* __restrict__ x, int M, int K, const int32_t* __restrict__ idx, int k,
@@ -187,12 +171,6 @@ __global__ void k_wg_reduce(const float* __restrict__ part, int splits, size_t n
 // write fp32 partials that a second kernel adds in split order (repeat calls: identical bits).
 constexpr int kIwTok = 64, kIwCols = 32, kIwRows = 32, kIwThreads = 128, kIwStages = 4;
 constexpr int kIwDyLd = kIwRows + 8, kIwWLd = kIwCols + 8;   // padded row strides (halves)
-
-__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], const void* p) {
-  const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
-}
 
 // grid (M / 64, k_ld / 32, row splits of `per` rows, a multiple of 32); N % 8 == 0
 __global__ void __launch_bounds__(kIwThreads)
