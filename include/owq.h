@@ -370,6 +370,106 @@ owq_status_t owq_weak_grad(owq_layer_t layer, const uint16_t* x, const uint16_t*
 owq_status_t owq_input_grad(owq_layer_t layer, const uint16_t* dy, uint16_t* dx, int M,
                             owq_stream_t stream);
 
+/* Activations of the gated block. */
+#define OWQ_ACT_SILU       0   /* g / (1 + e^-g)                                              */
+#define OWQ_ACT_GELU       1   /* g (1 + erf(g / sqrt 2)) / 2                                 */
+#define OWQ_ACT_GELU_TANH  2   /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2             */
+
+/*
+ * The gated block of a decoder's feed-forward part over two packed layers of one shape that
+ * share their input (the pages' LLaMA layers: gate and up):
+ *   g = x Wg^T,  u = x Wu^T,  h = act(g) * u
+ * with W the dequantised weight W_hat = fp16_rn(s (q - z)) itself, bit-exact at every M, and the
+ * weak columns in fp16.  g and u stay in fp32 and are not written; h is rounded once.
+ * Rules of all gated calls: `gate` and `up` are live handles with the same N, K (OWQ_ERR_SHAPE),
+ * bits (OWQ_ERR_BITS) and group (OWQ_ERR_GROUP), packed on the current device
+ * (OWQ_ERR_DEVICE); their weak columns may differ, and they may be the same handle.  Nothing is
+ * kept in the handles: calls on any streams may overlap and may be captured, as long as their
+ * outputs and workspaces do not.  x, dh and so on are row-major and contiguous; outputs are
+ * fully overwritten and must not overlap inputs.  Waits are bounded (OWQ_ERR_TIMEOUT through
+ * owq_device_status; outputs are then undefined).  Repeated calls give identical bits.
+ */
+
+/*
+ * owq_gated_gemv -- h for 1 <= M <= 16 tokens in one launch, bound by reading the packed
+ * weights once.  In: x fp16 M x K.  Out: h fp16 M x N.  No workspace.
+ */
+owq_status_t owq_gated_gemv(owq_layer_t gate, owq_layer_t up, int act, const uint16_t* x,
+                            uint16_t* h, int M, owq_stream_t stream);
+
+/*
+ * owq_gated_workspace -- bytes of workspace that owq_gated_gemm, owq_gated_grad and
+ * owq_gated_input_grad each need at most for M tokens (host call; 1 <= M <= 65536).  The
+ * workspace needs no initialisation and carries nothing from one call to the next.
+ */
+owq_status_t owq_gated_workspace(owq_layer_t gate, owq_layer_t up, int M, size_t* bytes);
+
+/*
+ * owq_gated_gemm -- h for any M (1..65536) on the 5th-generation tensor cores (tuned for
+ * M >= 64).  ws: device workspace of ws_bytes (OWQ_ERR_NOMEM if it is too small).
+ */
+owq_status_t owq_gated_gemm(owq_layer_t gate, owq_layer_t up, int act, const uint16_t* x,
+                            uint16_t* h, int M, void* ws, size_t ws_bytes, owq_stream_t stream);
+
+/*
+ * owq_gated_grad -- backward through the activation and the product, with g and u recomputed
+ * from x (so the forward keeps nothing but x):
+ *   dup = dh * act(g),   dgate = dh * u * act'(g)
+ * In: x fp16 M x K, dh fp16 M x N (the gradient of h).  Out: dgate, dup fp16 M x N, the
+ * gradients of both projections' outputs, each rounded once: what owq_gated_input_grad and
+ * owq_weak_grad (per layer) take.  Workspace as owq_gated_gemm.
+ */
+owq_status_t owq_gated_grad(owq_layer_t gate, owq_layer_t up, int act, const uint16_t* x,
+                            const uint16_t* dh, uint16_t* dgate, uint16_t* dup, int M, void* ws,
+                            size_t ws_bytes, owq_stream_t stream);
+
+/*
+ * owq_gated_input_grad -- dx = dgate Wg + dup Wu (M x K), W with the weak columns' fp16 values;
+ * both terms in one fp32 accumulator, rounded once.  In: dgate, dup fp16 M x N.  Any N and
+ * 1 <= M <= 65536 (N % 8 != 0: the gradients are first copied to padded rows of the workspace).
+ */
+owq_status_t owq_gated_input_grad(owq_layer_t gate, owq_layer_t up, const uint16_t* dgate,
+                                  const uint16_t* dup, uint16_t* dx, int M, void* ws,
+                                  size_t ws_bytes, owq_stream_t stream);
+
+/* Gradient tensors of owq_clip_create: n contiguous values of `dtype` (device pointers, aligned
+ * to the value's size; out may equal grad: in place; both may be NULL when n == 0). */
+#define OWQ_F32   0
+#define OWQ_F16   1
+#define OWQ_BF16  2
+typedef struct {
+  const void* grad;
+  void* out;
+  long long n;
+  int dtype;
+} owq_grad_t;
+/* Opaque list of gradient tensors; owns a device table of their addresses. */
+typedef struct owq_clip_s* owq_clip_t;
+
+/*
+ * owq_clip_create -- the list of tensors a fine-tuning step clips together (the weak blocks'
+ * gradients of all layers, say).  `grads` is a HOST array of `count` (0..2^20) entries.  No
+ * value that one entry writes may lie in another entry's ranges or, unless out == grad, in its
+ * own input (OWQ_ERR_ARG).  The tensors must outlive the handle's calls.  Allocates the table
+ * and synchronises `stream`.
+ */
+owq_status_t owq_clip_create(const owq_grad_t* grads, int count, owq_stream_t stream, owq_clip_t* out);
+
+/*
+ * owq_clip_grads -- *norm = sqrt(sum of the squares of all values) (device fp32, squares added in
+ * fp64) and out = grad * min(1, *norm finite ? max_norm / (*norm + 1e-6) : 1) for every tensor,
+ * multiplied in fp32 and rounded once.  A norm that is not finite clips nothing: the caller
+ * reads it and skips the step.  In place and unclipped, nothing is written.  max_norm >= 0
+ * (infinity: the norm alone; OWQ_ERR_ARG for negative or NaN).  One cooperative launch, allowed
+ * in a capture.  Calls on one handle must be ordered (they share its partial sums); the handle
+ * belongs to the device it was created on (OWQ_ERR_DEVICE).  A bounded wait that gives up
+ * leaves the outputs undefined.  Repeated calls give identical bits.
+ */
+owq_status_t owq_clip_grads(owq_clip_t clip, float max_norm, float* norm, owq_stream_t stream);
+
+/* Release a list (NULL is a no-op); its calls must have finished. */
+owq_status_t owq_clip_free(owq_clip_t clip);
+
 /*
  * owq_dequant -- test hook: write W_hat = fp16_rn(s * (q - z)) (N x K fp16, 0 at the weak
  * columns) and, if codes is not NULL, the unpacked codes (N x K uint8).

@@ -23,6 +23,8 @@ STATUS_NAMES = {
     5: "OWQ_ERR_INDEX", 6: "OWQ_ERR_ALIGN", 7: "OWQ_ERR_CUDA", 8: "OWQ_ERR_TIMEOUT",
     9: "OWQ_ERR_NOMEM", 10: "OWQ_ERR_HANDLE", 11: "OWQ_ERR_DEVICE", 12: "OWQ_ERR_ARG", 13: "OWQ_ERR_BOUNDS",
 }
+OWQ_ACT_SILU, OWQ_ACT_GELU, OWQ_ACT_GELU_TANH = 0, 1, 2
+OWQ_F32, OWQ_F16, OWQ_BF16 = 0, 1, 2
 OWQ_INJECT_NONE, OWQ_INJECT_GEMV_TAG, OWQ_INJECT_GEMM_ARRIVE, OWQ_INJECT_BOUNDS = 0, 1, 2, 3
 
 # (name, restype, argtypes) of every exported symbol of include/owq.h
@@ -44,6 +46,14 @@ PROTOTYPES = [
     ("owq_gemm_plan", _I, [_I, _I, _I, _I, ctypes.POINTER(_I)]),
     ("owq_weak_grad", _I, [_P, _P, _P, _P, _I, _P]),
     ("owq_input_grad", _I, [_P, _P, _P, _I, _P]),
+    ("owq_gated_gemv", _I, [_P, _P, _I, _P, _P, _I, _P]),
+    ("owq_gated_workspace", _I, [_P, _P, _I, _SZ]),
+    ("owq_gated_gemm", _I, [_P, _P, _I, _P, _P, _I, _P, ctypes.c_size_t, _P]),
+    ("owq_gated_grad", _I, [_P, _P, _I, _P, _P, _P, _P, _I, _P, ctypes.c_size_t, _P]),
+    ("owq_gated_input_grad", _I, [_P, _P, _P, _P, _P, _I, _P, ctypes.c_size_t, _P]),
+    ("owq_clip_create", _I, [_P, _I, _P, ctypes.POINTER(_P)]),
+    ("owq_clip_grads", _I, [_P, ctypes.c_float, _P, _P]),
+    ("owq_clip_free", _I, [_P]),
     ("owq_dequant", _I, [_P, _P, _P, _P]),
     ("owq_layer_info", _I, [_P] + [ctypes.POINTER(_I)] * 5),
     ("owq_layer_bytes", _I, [_P, _SZ, _SZ, _SZ, _SZ]),
@@ -189,6 +199,50 @@ def owq_weak_grad(layer, x, dy, dw_weak, M, stream=None) -> int:
 
 def owq_input_grad(layer, dy, dx, M, stream=None) -> int:
     return LIB.owq_input_grad(layer, _ptr(dy), _ptr(dx), M, _stream(stream))
+
+
+def owq_gated_gemv(gate, up, act, x, h, M, stream=None) -> int:
+    return LIB.owq_gated_gemv(gate, up, act, _ptr(x), _ptr(h), M, _stream(stream))
+
+
+def owq_gated_workspace(gate, up, M):
+    """Returns (status, bytes)."""
+    n = ctypes.c_size_t()
+    st = LIB.owq_gated_workspace(gate, up, M, ctypes.byref(n))
+    return st, n.value
+
+
+def owq_gated_gemm(gate, up, act, x, h, M, ws, ws_bytes, stream=None) -> int:
+    return LIB.owq_gated_gemm(gate, up, act, _ptr(x), _ptr(h), M, _ptr(ws), ws_bytes, _stream(stream))
+
+
+def owq_gated_grad(gate, up, act, x, dh, dgate, dup, M, ws, ws_bytes, stream=None) -> int:
+    return LIB.owq_gated_grad(gate, up, act, _ptr(x), _ptr(dh), _ptr(dgate), _ptr(dup), M, _ptr(ws), ws_bytes,
+                              _stream(stream))
+
+
+def owq_gated_input_grad(gate, up, dgate, dup, dx, M, ws, ws_bytes, stream=None) -> int:
+    return LIB.owq_gated_input_grad(gate, up, _ptr(dgate), _ptr(dup), _ptr(dx), M, _ptr(ws), ws_bytes, _stream(stream))
+
+
+class OwqGrad(ctypes.Structure):
+    """owq_grad_t: one gradient tensor of owq_clip_create."""
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_longlong), ("dtype", ctypes.c_int)]
+
+
+def owq_clip_create(grads, count, stream=None):
+    """grads: a ctypes array of OwqGrad (or None).  Returns (status, handle)."""
+    h = ctypes.c_void_p()
+    st = LIB.owq_clip_create(grads, count, _stream(stream), ctypes.byref(h))
+    return st, h.value
+
+
+def owq_clip_grads(clip, max_norm, norm, stream=None) -> int:
+    return LIB.owq_clip_grads(clip, float(max_norm), _ptr(norm), _stream(stream))
+
+
+def owq_clip_free(clip) -> int:
+    return LIB.owq_clip_free(clip)
 
 
 def owq_dequant(layer, w_hat, codes=None, stream=None) -> int:
@@ -341,3 +395,176 @@ def quantize_pack(W, X, bits: int, group: int, k: int, stream=None) -> tuple[Owq
     q = quantize(W, X, bits, group, k, stream)
     layer = OwqLayer(q["codes"], q["scales"], q["zeros"], q["idx"], q["w_weak"], bits, group, stream)
     return layer, q
+
+
+def _check_tensor(t, name: str, shape, dtype, device=None) -> None:
+    """A contiguous CUDA tensor of this shape and type (ValueError otherwise)."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def _run_on(device, stream, fn):
+    """fn(stream handle) with `device` current and, for an explicit stream (a torch stream or a
+    raw handle), that stream current too, so that what fn allocates belongs to it."""
+    import torch
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _run_on(device, stream, fn)
+    if stream is None:
+        return fn(torch.cuda.current_stream().cuda_stream)
+    ext = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    with torch.cuda.stream(ext):
+        return fn(ext.cuda_stream)
+
+
+class OwqGated:
+    """The gated block h = act(x Wg^T) * (x Wu^T) of two packed layers of one shape (see
+    owq_gated_gemv and the calls after it in include/owq.h), with its backward pass.  act:
+    "silu", "gelu" (erf) or "gelu_tanh".  Nothing is kept between calls; tensors are fp16,
+    contiguous, on the layers' device, and a given output or `stream` is used as it is."""
+
+    ACTS = {"silu": OWQ_ACT_SILU, "gelu": OWQ_ACT_GELU, "gelu_tanh": OWQ_ACT_GELU_TANH}
+
+    def __init__(self, gate: OwqLayer, up: OwqLayer, act: str = "silu"):
+        if act not in self.ACTS:
+            raise ValueError(f"act {act!r}: expected one of {sorted(self.ACTS)}")
+        for what in ("N", "K", "bits", "group"):
+            if getattr(gate, what) != getattr(up, what):
+                raise ValueError(f"gate and up differ in {what}: {getattr(gate, what)} and {getattr(up, what)}")
+        self.gate, self.up, self.act = gate, up, self.ACTS[act]
+        self.N, self.K = gate.N, gate.K
+
+    def _rows(self, t, name: str, width: int) -> int:
+        import torch
+        if t.dim() != 2:
+            raise ValueError(f"{name}: expected 2 dimensions, got {tuple(t.shape)}")
+        _check_tensor(t, name, (t.shape[0], width), torch.float16)
+        return t.shape[0]
+
+    def _out(self, t, name: str, M: int, width: int, like):
+        import torch
+        if t is None:
+            return torch.empty((M, width), dtype=torch.float16, device=like.device)
+        _check_tensor(t, name, (M, width), torch.float16, like.device)
+        return t
+
+    def _workspace(self, M: int, device):
+        import torch
+        st, n = owq_gated_workspace(self.gate.handle, self.up.handle, M)
+        _check(st, "owq_gated_workspace")
+        return torch.empty(n, dtype=torch.uint8, device=device), n
+
+    def gemv(self, x, h=None, stream=None):
+        """h for 1 to 16 tokens (x: M x K)."""
+        M = self._rows(x, "x", self.K)
+
+        def go(s):
+            y = self._out(h, "h", M, self.N, x)
+            _check(LIB.owq_gated_gemv(self.gate.handle, self.up.handle, self.act, x.data_ptr(), y.data_ptr(), M, s),
+                   "owq_gated_gemv")
+            return y
+        return _run_on(x.device, stream, go)
+
+    def gemm(self, x, h=None, stream=None):
+        """h for any number of tokens (tuned for 64 and more)."""
+        M = self._rows(x, "x", self.K)
+
+        def go(s):
+            ws, n = self._workspace(M, x.device)
+            y = self._out(h, "h", M, self.N, x)
+            _check(owq_gated_gemm(self.gate.handle, self.up.handle, self.act, x, y, M, ws, n, s), "owq_gated_gemm")
+            return y
+        return _run_on(x.device, stream, go)
+
+    def grad(self, x, dh, dgate=None, dup=None, stream=None):
+        """(dgate, dup): the gradients of x Wg^T and x Wu^T, recomputed from x."""
+        M = self._rows(x, "x", self.K)
+        _check_fp16(dh, "dh", (M, self.N), x.device)
+
+        def go(s):
+            ws, n = self._workspace(M, x.device)
+            g, u = self._out(dgate, "dgate", M, self.N, x), self._out(dup, "dup", M, self.N, x)
+            _check(owq_gated_grad(self.gate.handle, self.up.handle, self.act, x, dh, g, u, M, ws, n, s), "owq_gated_grad")
+            return g, u
+        return _run_on(x.device, stream, go)
+
+    def input_grad(self, dgate, dup, dx=None, stream=None):
+        """dx = dgate Wg + dup Wu."""
+        M = self._rows(dgate, "dgate", self.N)
+        _check_fp16(dup, "dup", (M, self.N), dgate.device)
+
+        def go(s):
+            ws, n = self._workspace(M, dgate.device)
+            d = self._out(dx, "dx", M, self.K, dgate)
+            _check(owq_gated_input_grad(self.gate.handle, self.up.handle, dgate, dup, d, M, ws, n, s), "owq_gated_input_grad")
+            return d
+        return _run_on(dgate.device, stream, go)
+
+    def backward(self, x, dh, dx=None, dgate=None, dup=None, stream=None):
+        """(dx, dgate, dup) from the gradient dh of h.  The weak blocks' gradients follow with
+        gate.weak_grad(x, dgate) and up.weak_grad(x, dup)."""
+        g, u = self.grad(x, dh, dgate, dup, stream)
+        return self.input_grad(g, u, dx, stream), g, u
+
+
+def _check_fp16(t, name: str, shape, device) -> None:
+    import torch
+    _check_tensor(t, name, shape, torch.float16, device)
+
+
+class OwqGradClip:
+    """The gradient tensors that a step clips together (see owq_clip_create in include/owq.h):
+    fp32, fp16 or bf16, contiguous, on one device.  `outs` takes the clipped values (None: in
+    place).  Calling it with max_norm returns the global norm, a device tensor of one fp32."""
+
+    def __init__(self, grads, outs=None, stream=None):
+        import torch
+        self.handle = None
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        kinds = {torch.float32: OWQ_F32, torch.float16: OWQ_F16, torch.bfloat16: OWQ_BF16}
+        if len(self.outs) != len(self.grads):
+            raise ValueError(f"{len(self.grads)} gradients and {len(self.outs)} outputs")
+        self.device = self.grads[0].device if self.grads else torch.device("cuda", torch.cuda.current_device())
+        table = (OwqGrad * max(1, len(self.grads)))()
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            if g.dtype not in kinds:
+                raise ValueError(f"gradient {i}: {g.dtype}, expected float32, float16 or bfloat16")
+            _check_tensor(g, f"gradient {i}", g.shape, g.dtype, self.device)
+            if o is not g:
+                _check_tensor(o, f"output {i}", g.shape, g.dtype, self.device)
+            table[i] = OwqGrad(g.data_ptr(), o.data_ptr(), g.numel(), kinds[g.dtype])
+        st, self.handle = _run_on(self.device, stream, lambda s: owq_clip_create(table, len(self.grads), s))
+        _check(st, "owq_clip_create")
+
+    def __call__(self, max_norm: float, norm=None, stream=None):
+        import torch
+
+        def go(s):
+            n = torch.empty(1, dtype=torch.float32, device=self.device) if norm is None else norm
+            _check_tensor(n, "norm", (1,), torch.float32, self.device)
+            _check(owq_clip_grads(self.handle, max_norm, n, s), "owq_clip_grads")
+            return n
+        return _run_on(self.device, stream, go)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            owq_clip_free(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def clip_grads(grads, max_norm: float, outs=None, stream=None):
+    """OwqGradClip for one call: returns the norm (synchronises: the list is made and released)."""
+    clip = OwqGradClip(grads, outs, stream)
+    norm = clip(max_norm, stream=stream)
+    clip.close()
+    return norm

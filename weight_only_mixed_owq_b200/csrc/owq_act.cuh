@@ -1,0 +1,44 @@
+// Activations of the gated feed-forward block, a(g) and a'(g), in fp32.
+//   silu       a = g s,  s = 1 / (1 + e^-g);                     a' = s (1 + g (1 - s))
+//   gelu       a = g P,  P = erfc(-g / sqrt 2) / 2;              a' = P + g e^(-g^2/2) / sqrt(2 pi)
+//   gelu_tanh  a = g s,  s = 1 / (1 + e^-2v) = (1 + tanh v) / 2, v = sqrt(2/pi) (g + 0.044715 g^3);
+//              a' = s + 2 g s (1 - s) v'
+// The erfc and logistic forms keep the relative accuracy of the small values at large negative
+// g, where 1 + erf and 1 + tanh cancel; e^x overflowing to infinity gives s = 0, as it should.
+#pragma once
+#include "owq_internal.cuh"
+
+namespace owq {
+
+template <int ACT>
+__device__ __forceinline__ void act_eval(float g, float& a, float& da) {
+  if constexpr (ACT == OWQ_ACT_SILU) {
+    const float s = 1.f / (1.f + expf(-g));
+    a = g * s;
+    da = s * (1.f + g * (1.f - s));
+  } else if constexpr (ACT == OWQ_ACT_GELU) {
+    const float p = 0.5f * erfcf(-g * 0.70710678118654752f);
+    a = g * p;
+    da = p + g * (expf(-0.5f * g * g) * 0.39894228040143268f);
+  } else {
+    constexpr float c = 0.79788456080286536f, k = 0.044715f;
+    const float g2 = g * g;
+    const float s = 1.f / (1.f + expf(-2.f * c * (g + k * g2 * g)));
+    a = g * s;
+    da = s + g * (s * (1.f - s)) * (2.f * c * (1.f + 3.f * k * g2));
+  }
+}
+__device__ __forceinline__ float act_value(int act, float g) {
+  float a, da;
+  if (act == OWQ_ACT_SILU) act_eval<OWQ_ACT_SILU>(g, a, da);
+  else if (act == OWQ_ACT_GELU) act_eval<OWQ_ACT_GELU>(g, a, da);
+  else act_eval<OWQ_ACT_GELU_TANH>(g, a, da);
+  return a;
+}
+__device__ __forceinline__ void act_both(int act, float g, float& a, float& da) {
+  if (act == OWQ_ACT_SILU) act_eval<OWQ_ACT_SILU>(g, a, da);
+  else if (act == OWQ_ACT_GELU) act_eval<OWQ_ACT_GELU>(g, a, da);
+  else act_eval<OWQ_ACT_GELU_TANH>(g, a, da);
+}
+
+}  // namespace owq

@@ -1,6 +1,8 @@
 // C ABI of the library (declared in include/owq.h): argument validation, layer handles,
 // launches.  Every argument is validated on the host before anything is launched.
 #include <algorithm>
+#include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <new>
@@ -19,6 +21,21 @@ int* device_status_ptr() {
   return p;
 }
 
+int layer_sm_count(int dev) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> n[kMaxDev];
+  if (dev < 0 || dev >= kMaxDev) return 148;
+  int v = n[dev].load(std::memory_order_relaxed);
+  if (!v) {
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) {
+      cudaGetLastError();
+      v = 148;
+    }
+    n[dev].store(v, std::memory_order_relaxed);
+  }
+  return v;
+}
+
 namespace {
 
 std::mutex g_mu;
@@ -32,6 +49,40 @@ Layer* lookup(owq_layer_t h) {
   if (!L) return nullptr;
   std::lock_guard<std::mutex> g(g_mu);
   return registry().count(L) ? L : nullptr;
+}
+
+std::unordered_set<Clip*>& clip_registry() {
+  static std::unordered_set<Clip*> s;
+  return s;
+}
+
+Clip* lookup_clip(owq_clip_t h) {
+  Clip* c = reinterpret_cast<Clip*>(h);
+  if (!c) return nullptr;
+  std::lock_guard<std::mutex> g(g_mu);
+  return clip_registry().count(c) ? c : nullptr;
+}
+
+void release_clip(Clip* c) {
+  cudaFree(c->chunks);
+  cudaFree(c->part);
+  delete c;
+}
+
+// The two layers of a gated block: live handles of one shape and layout, on the current device.
+owq_status_t lookup_pair(owq_layer_t gate, owq_layer_t up, Layer** g, Layer** u) {
+  *g = lookup(gate);
+  *u = lookup(up);
+  if (!*g || !*u) return OWQ_ERR_HANDLE;
+  if ((*g)->bits != (*u)->bits) return OWQ_ERR_BITS;
+  if ((*g)->N != (*u)->N || (*g)->K != (*u)->K) return OWQ_ERR_SHAPE;
+  if ((*g)->group != (*u)->group) return OWQ_ERR_GROUP;
+  return OWQ_OK;
+}
+owq_status_t check_pair_device(const Layer* g, const Layer* u) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) { cudaGetLastError(); return OWQ_ERR_DEVICE; }
+  return g->device == dev && u->device == dev ? OWQ_OK : OWQ_ERR_DEVICE;
 }
 
 owq_status_t check_device() {
@@ -508,6 +559,168 @@ owq_status_t owq_input_grad(owq_layer_t layer, const uint16_t* dy, uint16_t* dx,
     return cuda_status(launch_input_grad_weak(*L, dyh, dxh, M, inject, s));
   }
   return cuda_status(launch_input_grad(*L, dyh, dxh, M, s));
+}
+
+owq_status_t owq_gated_gemv(owq_layer_t gate, owq_layer_t up, int act, const uint16_t* x, uint16_t* h, int M,
+                            owq_stream_t stream) {
+  Layer *g, *u;
+  owq_status_t st = lookup_pair(gate, up, &g, &u);
+  if (st) return st;
+  if (act < OWQ_ACT_SILU || act > OWQ_ACT_GELU_TANH) return OWQ_ERR_ARG;
+  if (M < 1 || M > kMaxGemvM) return OWQ_ERR_SHAPE;
+  if (!x || !h) return OWQ_ERR_NULL;
+  if (!aligned16(x) || !aligned16(h)) return OWQ_ERR_ALIGN;
+  if ((st = check_pair_device(g, u))) return st;
+  return cuda_status(launch_gated_gemv(*g, *u, act, reinterpret_cast<const __half*>(x), reinterpret_cast<__half*>(h), M,
+                                       kDefaultWaitLimit, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+owq_status_t owq_gated_workspace(owq_layer_t gate, owq_layer_t up, int M, size_t* bytes) {
+  Layer *g, *u;
+  owq_status_t st = lookup_pair(gate, up, &g, &u);
+  if (st) return st;
+  if (!bytes) return OWQ_ERR_NULL;
+  if (M < 1 || M > 65536) return OWQ_ERR_SHAPE;
+  *bytes = std::max<size_t>(256, std::max(gated_gemm_ws_bytes(*g, *u, M), gated_input_grad_ws_bytes(*g, *u, M)));
+  return OWQ_OK;
+}
+
+owq_status_t owq_gated_gemm(owq_layer_t gate, owq_layer_t up, int act, const uint16_t* x, uint16_t* h, int M, void* ws,
+                            size_t ws_bytes, owq_stream_t stream) {
+  Layer *g, *u;
+  owq_status_t st = lookup_pair(gate, up, &g, &u);
+  if (st) return st;
+  if (act < OWQ_ACT_SILU || act > OWQ_ACT_GELU_TANH) return OWQ_ERR_ARG;
+  if (M < 1 || M > 65536) return OWQ_ERR_SHAPE;
+  if (!x || !h || !ws) return OWQ_ERR_NULL;
+  if (!aligned16(x) || !aligned16(h) || !aligned16(ws)) return OWQ_ERR_ALIGN;
+  if ((st = check_pair_device(g, u))) return st;
+  long long wl;
+  const bool skip = take_inject(OWQ_INJECT_GEMM_ARRIVE, &wl);
+  return gated_gemm_sm100(*g, *u, act, reinterpret_cast<const __half*>(x), nullptr, reinterpret_cast<__half*>(h), nullptr, M, ws,
+                          ws_bytes, wl, skip, reinterpret_cast<cudaStream_t>(stream));
+}
+
+owq_status_t owq_gated_grad(owq_layer_t gate, owq_layer_t up, int act, const uint16_t* x, const uint16_t* dh, uint16_t* dgate,
+                            uint16_t* dup, int M, void* ws, size_t ws_bytes, owq_stream_t stream) {
+  Layer *g, *u;
+  owq_status_t st = lookup_pair(gate, up, &g, &u);
+  if (st) return st;
+  if (act < OWQ_ACT_SILU || act > OWQ_ACT_GELU_TANH) return OWQ_ERR_ARG;
+  if (M < 1 || M > 65536) return OWQ_ERR_SHAPE;
+  if (!x || !dh || !dgate || !dup || !ws) return OWQ_ERR_NULL;
+  if (!aligned16(x) || !aligned16(dh) || !aligned16(dgate) || !aligned16(dup) || !aligned16(ws)) return OWQ_ERR_ALIGN;
+  if ((st = check_pair_device(g, u))) return st;
+  return gated_gemm_sm100(*g, *u, act, reinterpret_cast<const __half*>(x), reinterpret_cast<const __half*>(dh),
+                          reinterpret_cast<__half*>(dgate), reinterpret_cast<__half*>(dup), M, ws, ws_bytes, kDefaultWaitLimit,
+                          false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+owq_status_t owq_gated_input_grad(owq_layer_t gate, owq_layer_t up, const uint16_t* dgate, const uint16_t* dup, uint16_t* dx,
+                                  int M, void* ws, size_t ws_bytes, owq_stream_t stream) {
+  Layer *g, *u;
+  owq_status_t st = lookup_pair(gate, up, &g, &u);
+  if (st) return st;
+  if (M < 1 || M > 65536) return OWQ_ERR_SHAPE;
+  if (!dgate || !dup || !dx || !ws) return OWQ_ERR_NULL;
+  if (!aligned16(dgate) || !aligned16(dup) || !aligned16(dx) || !aligned16(ws)) return OWQ_ERR_ALIGN;
+  if ((st = check_pair_device(g, u))) return st;
+  return gated_input_grad_sm100(*g, *u, reinterpret_cast<const __half*>(dgate), reinterpret_cast<const __half*>(dup),
+                                reinterpret_cast<__half*>(dx), M, ws, ws_bytes, kDefaultWaitLimit,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+owq_status_t owq_clip_create(const owq_grad_t* grads, int count, owq_stream_t stream, owq_clip_t* out) {
+  if (!out) return OWQ_ERR_NULL;
+  *out = nullptr;
+  if (count < 0 || count > (1 << 20)) return OWQ_ERR_SHAPE;
+  if (count > 0 && !grads) return OWQ_ERR_NULL;
+  struct Range { uintptr_t lo, hi; int tensor; bool write; };
+  std::vector<Range> ranges;
+  long long total = 0;
+  for (int i = 0; i < count; ++i) {
+    const owq_grad_t& t = grads[i];
+    if (t.dtype != OWQ_F32 && t.dtype != OWQ_F16 && t.dtype != OWQ_BF16) return OWQ_ERR_ARG;
+    if (t.n < 0 || t.n > (1LL << 40)) return OWQ_ERR_SHAPE;
+    if (t.n == 0) continue;
+    if (!t.grad || !t.out) return OWQ_ERR_NULL;
+    const uintptr_t size = t.dtype == OWQ_F32 ? 4 : 2, in = (uintptr_t)t.grad, o = (uintptr_t)t.out, bytes = size * (uintptr_t)t.n;
+    if (in % size || o % size) return OWQ_ERR_ALIGN;
+    ranges.push_back({in, in + bytes, i, o == in});
+    if (o != in) ranges.push_back({o, o + bytes, i, true});
+    total += (long long)bytes;
+  }
+  // a value that one tensor writes is in no other range (two reads of the same values may overlap)
+  std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  uintptr_t read_end = 0, write_end = 0;
+  for (const Range& r : ranges) {
+    if (r.lo < write_end || (r.write && r.lo < read_end)) return OWQ_ERR_ARG;
+    (r.write ? write_end : read_end) = std::max(r.write ? write_end : read_end, r.hi);
+  }
+  owq_status_t st = check_device();
+  if (st) return st;
+  Clip* c = new (std::nothrow) Clip();
+  if (!c) return OWQ_ERR_NOMEM;
+  cudaGetDevice(&c->device);
+  c->chunks = nullptr;
+  c->part = nullptr;
+  const int sms = layer_sm_count(c->device);
+  c->chunk_bytes = clip_chunk_bytes(total, sms);
+  std::vector<ClipChunk> table;
+  for (int i = 0; i < count; ++i) {
+    const owq_grad_t& t = grads[i];
+    const long long size = t.dtype == OWQ_F32 ? 4 : 2;
+    const char* in = static_cast<const char*>(t.grad);
+    char* o = static_cast<char*>(t.out);
+    for (long long at = 0; at < t.n;) {   // chunks end where the input is 16-byte aligned
+      long long n = (c->chunk_bytes - (long long)((uintptr_t)(in + at * size) & 15)) / size;
+      n = std::min(n, t.n - at);
+      table.push_back({in + at * size, o + at * size, (int)n, t.dtype});
+      at += n;
+      if (table.size() > (size_t)1 << 30) { delete c; return OWQ_ERR_SHAPE; }
+    }
+  }
+  c->n_chunks = (int)table.size();
+  c->grid = std::max(1, std::min(sms, c->n_chunks));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMalloc(&c->chunks, std::max<size_t>(1, table.size()) * sizeof(ClipChunk));
+  if (e == cudaSuccess) e = cudaMalloc(&c->part, (c->grid + 1) * sizeof(double));
+  if (e == cudaSuccess) {
+    c->arrived = reinterpret_cast<unsigned long long*>(c->part + c->grid);
+    e = cudaMemsetAsync(c->part, 0, (c->grid + 1) * sizeof(double), s);
+  }
+  if (e == cudaSuccess && c->n_chunks > 0)
+    e = cudaMemcpyAsync(c->chunks, table.data(), table.size() * sizeof(ClipChunk), cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);   // the host table must outlive its copy
+  if (e != cudaSuccess) { release_clip(c); return cuda_status(e); }
+  {
+    std::lock_guard<std::mutex> g(g_mu);
+    clip_registry().insert(c);
+  }
+  *out = reinterpret_cast<owq_clip_t>(c);
+  return OWQ_OK;
+}
+
+owq_status_t owq_clip_grads(owq_clip_t clip, float max_norm, float* norm, owq_stream_t stream) {
+  Clip* c = lookup_clip(clip);
+  if (!c) return OWQ_ERR_HANDLE;
+  if (!(max_norm >= 0.f)) return OWQ_ERR_ARG;
+  if (!norm) return OWQ_ERR_NULL;
+  if (!aligned16(norm)) return OWQ_ERR_ALIGN;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != c->device) { cudaGetLastError(); return OWQ_ERR_DEVICE; }
+  return cuda_status(launch_clip(*c, max_norm, norm, kDefaultWaitLimit, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+owq_status_t owq_clip_free(owq_clip_t clip) {
+  if (!clip) return OWQ_OK;
+  Clip* c = reinterpret_cast<Clip*>(clip);
+  {
+    std::lock_guard<std::mutex> g(g_mu);
+    if (!clip_registry().erase(c)) return OWQ_ERR_HANDLE;
+  }
+  release_clip(c);
+  return OWQ_OK;
 }
 
 owq_status_t owq_dequant(owq_layer_t layer, uint16_t* w_hat, uint8_t* codes, owq_stream_t stream) {

@@ -181,4 +181,37 @@ GemmPlan gemm_plan(int N, int K, int M, int sms);
 owq_status_t gemm_sm100(Layer& L, const __half* x, __half* y, int M, long long wait_limit,
                         bool skip_arrive, cudaStream_t s);
 
+// ---- gated block (two layers of one shape that share their input) ----
+// decode form, M <= kMaxGemvM: one launch, no workspace
+cudaError_t launch_gated_gemv(const Layer& gate, const Layer& up, int act, const __half* x, __half* h, int M,
+                              long long wait_limit, cudaStream_t s);
+// many tokens: h = act(g) u (dh NULL, out0 = h), or the gradients of both projections' outputs
+// (out0 = dg, out1 = du); ws: the caller's workspace of at least gated_gemm_ws_bytes
+size_t gated_gemm_ws_bytes(const Layer& gate, const Layer& up, int M);
+owq_status_t gated_gemm_sm100(const Layer& gate, const Layer& up, int act, const __half* x, const __half* dh, __half* out0,
+                              __half* out1, int M, void* ws, size_t ws_bytes, long long wait_limit, bool skip_arrive,
+                              cudaStream_t s);
+// dx = dg Wg + du Wu
+size_t gated_input_grad_ws_bytes(const Layer& gate, const Layer& up, int M);
+owq_status_t gated_input_grad_sm100(const Layer& gate, const Layer& up, const __half* dg, const __half* du, __half* dx, int M,
+                                    void* ws, size_t ws_bytes, long long wait_limit, cudaStream_t s);
+// SM count of device `dev` (cached per device ordinal)
+int layer_sm_count(int dev);
+
+// ---- gradient clipping ----
+struct ClipChunk {   // at most chunk_bytes / element size consecutive values of one tensor
+  const void* in;
+  void* out;
+  int n, dtype;
+};
+struct Clip {
+  int device;
+  ClipChunk* chunks;             // device table
+  int n_chunks, chunk_bytes, grid;
+  double* part;                  // [grid] partial sums
+  unsigned long long* arrived;   // CTAs that have published their sum, over all calls
+};
+int clip_chunk_bytes(long long total_bytes, int sms);
+cudaError_t launch_clip(const Clip& c, float max_norm, float* norm, long long wait_limit, cudaStream_t s);
+
 }  // namespace owq
