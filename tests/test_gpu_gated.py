@@ -97,6 +97,8 @@ GEMM = [(s, M) for s in SHAPES[:6] for M in (1, 17, 64, 65, 200, 300)] + [
     ((200, 2048, 4, 2048, 16, 70), 150),
     ((2470, 4096, 3, 128, 8, 8), 769),
     ((2371, 640, 4, 640, 0, 33), 1030),
+    ((70, 128, 3, 128, 128, 128), 300),   # every column weak in both layers
+    ((70, 128, 4, 128, 128, 127), 100),
 ]
 
 

@@ -25,6 +25,38 @@ namespace {
 using namespace sm100;
 
 constexpr int kHalfRows = kBM / 2;     // output rows of a tile: 64 of each layer
+constexpr int kDW = 16;                // A-operand warps
+#ifndef OWQ_GR256
+#define OWQ_GR256 2
+#endif
+
+// How the tiles of a product become CTAs: `whole` tiles take one CTA each; each of the others is
+// split `splits` ways over its steps (`steps` a split).  CTAs are dispatched in index order, so the
+// split tiles run last.  The plain order would leave the last wave short: T tiles on P SMs take
+// ceil(T / P) tile times, with the last T mod P of them split over the idle SMs about T / P.
+struct TileSplit {
+  int tiles, whole, splits, steps;
+  int ctas() const { return whole + (tiles - whole) * splits; }
+};
+struct TileOf {   // a CTA's part
+  int tile, split, n_splits, first, steps;
+};
+__device__ __forceinline__ TileOf tile_of(const TileSplit& p, int cta, int all_steps) {
+  TileOf t = {cta, 0, 1, 0, all_steps};
+  if (cta >= p.whole) {
+    const int u = cta - p.whole;
+    t.tile = p.whole + u / p.splits;
+    t.split = u % p.splits;
+    t.n_splits = p.splits;
+    t.first = t.split * p.steps;
+    t.steps = max(0, min(p.steps, all_steps - t.first));
+  }
+  return t;
+}
+// fp32 partials of the split tiles: [split][tile - whole][token of the tile][MMA row]
+__device__ __forceinline__ size_t partial_at(const TileSplit& p, int split, int tile, int BN) {
+  return ((size_t)split * (p.tiles - p.whole) + (tile - p.whole)) * BN * kBM;
+}
 
 struct GatedMaps {
   CUtensorMap x, p[2], xw[2], sz[2];   // [0] gate, [1] up
@@ -36,14 +68,12 @@ struct GatedGemmParams {
   int k_ld[2];               // 0: no weak columns
   const __half* dh;          // NULL: forward
   __half* out[2];            // forward: h; backward: dg, du
-  float* ws;                 // split partials [split][gate, up][token - ws_t0][N]
-  size_t ws_plane;           // one plane, (M - ws_t0) N floats
-  int ws_t0;
+  float* ws;                 // split partials
   int* status;
   int N, K, M, G, act;
-  int ksteps;                           // dense steps per split (blockIdx.z)
-  int tail_y0, tail_sp, tail_ksteps;    // split tail, as in the prefill product
-  int nw;                               // weak steps: 64 columns of each layer's weak block
+  int rts;                   // row tiles (64 output rows each); tile = token tile * rts + row tile
+  TileSplit split;
+  int nw;                    // weak steps: 64 columns of each layer's weak block
   long long wait_limit;
   int skip_arrive;
 };
@@ -67,8 +97,10 @@ __device__ __forceinline__ void gated_store(const GatedGemmParams& p, size_t o, 
 // columns are finished by either lane.  Weak step w: columns 64 w .. 64 w + 63 of the gate's weak
 // block against its gathered activations in the first half of the step's K, the up layer's in the
 // second half, each with zeros in the other layer's rows.
-template <int BITS, int BN, int S, int DW, bool TAIL>
-__global__ void __launch_bounds__(32 * (2 + DW), 1)
+// The 16 A-operand warps work in GR groups on different steps (GR = 2: a warp's chain of barrier,
+// unpack and tensor-memory store for one step overlaps the other group's).
+template <int BITS, int BN, int S, int GR>
+__global__ void __launch_bounds__(32 * (2 + kDW), 1)
 k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ GatedGemmParams p) {
   using L = Smem<BITS, BN>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -81,28 +113,18 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int ty = blockIdx.y, sp = blockIdx.z, nsp = gridDim.z, ksteps = p.ksteps;
-  if constexpr (TAIL) {
-    if (ty >= p.tail_y0) {
-      const int u = ty - p.tail_y0;
-      ty = p.tail_y0 + u / p.tail_sp;
-      sp = u % p.tail_sp;
-      nsp = p.tail_sp;
-      ksteps = p.tail_ksteps;
-    }
-  }
-  const int n0 = blockIdx.x * kHalfRows;   // first output row
-  const int m0 = ty * BN;                  // first token
-  const int kb0 = sp * ksteps;
-  const int nD = max(0, min(ksteps, p.K / kStepCodes - kb0));   // dense steps of this split
-  const int nK = nD + (sp == nsp - 1 ? p.nw : 0);               // + the weak steps (last split)
+  const TileOf to = tile_of(p.split, blockIdx.x, p.K / kStepCodes);
+  const int n0 = (to.tile % p.rts) * kHalfRows;   // first output row
+  const int m0 = (to.tile / p.rts) * BN;          // first token
+  const int kb0 = to.first, nD = to.steps;        // dense steps of this split
+  const int nK = nD + (to.split == to.n_splits - 1 ? p.nw : 0);   // + the weak steps (last split)
   const bool per_group = p.G > 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&afull[s], 32 * DW);
+      mbar_init(&afull[s], 32 * kDW / GR);
     }
     mbar_init(accf, 1);
     fence_mbar_init();
@@ -111,6 +133,7 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
     prefetch_tmap(&maps.p[1]);
   }
   if (warp == 1) tmem_alloc(tmem_slot, tmem_cols<BN, S>());
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -139,6 +162,7 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
           tma_load_2d(st + BN * 128, &maps.x, &full[s], kb * kStepCodes + 64, m0);
         } else {
           const int c0 = (i - nD) * 64;
+          if (i == nD) asm volatile("griddepcontrol.wait;" ::: "memory");   // the gathered activations
           mbar_arrive_expect_tx(&full[s], L::kX);
           tma_load_2d(st, &maps.xw[0], &full[s], c0, m0);
           tma_load_2d(st + BN * 128, &maps.xw[1], &full[s], c0, m0);
@@ -181,10 +205,10 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
     }
   } else {
     // ---------------- A operand ----------------
-    // DW warps, NSL = DW / 4 per lane quarter; thread (MMA row r, slab jh) writes codes
-    // 8 U jh .. 8 U jh + 8 U - 1 of its row (U = 16 / NSL), as in the prefill kernel
-    constexpr int NSL = DW / 4, U = 16 / NSL;
-    const int quarter = warp & 3, jh = (warp - 2) >> 2;
+    // kDW / GR warps of a group, NSL = kDW / GR / 4 per lane quarter; thread (MMA row r, slab jh)
+    // writes codes 8 U jh .. 8 U jh + 8 U - 1 of its row (U = 16 / NSL), as in the prefill kernel
+    constexpr int NSL = kDW / GR / 4, U = 16 / NSL;
+    const int quarter = warp & 3, aw = warp - 2, grp = aw / (kDW / GR), jh = (aw % (kDW / GR)) >> 2;
     const int lay = lane >> 4, tr = 16 * quarter + (lane & 15);   // layer and row of the tile
     const int orow = n0 + tr;
     const int row = min(orow, p.N - 1);
@@ -203,7 +227,7 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
     };
     if (!per_group) set_sz(p.scales[lay][row], p.zeros[lay][row]);
     bool ok = true;
-    for (int i = 0; i < nK && ok; ++i) {
+    for (int i = grp; i < nK && ok; i += GR) {
       const int s = i % S, u = i / S;
       ok = mbar_wait(&full[s], u & 1, p.status, p.wait_limit);   // (also: the stage's previous MMAs are done)
       if (!ok) break;
@@ -263,21 +287,18 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
     // ---------------- epilogue ----------------
     const bool acc_ok = __all_sync(0xffffffffu, mbar_wait(accf, 0, p.status, p.wait_limit) && ok);
     tc_fence_after();
+    constexpr int kCols = BN / (kDW / 4);   // accumulator columns of this warp
+    const int col0 = (aw >> 2) * kCols;
     #pragma unroll 1
-    for (int c0 = jh * (BN / NSL); c0 < (jh + 1) * (BN / NSL); c0 += 16) {
+    for (int c0 = col0; c0 < col0 + kCols; c0 += 16) {
       uint32_t v[16];
       tmem_ld16(tmem + lane_base + (uint32_t)c0, v);
       tmem_ld_wait();
       if (!acc_ok) continue;
-      if (nsp > 1) {   // this split's fp32 partials
-        float* w = p.ws + ((size_t)sp * 2 + lay) * p.ws_plane;
-        if (orow < p.N) {
-          #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int t = m0 + c0 + j;
-            if (t < p.M) w[(size_t)(t - p.ws_t0) * p.N + orow] = __uint_as_float(v[j]);
-          }
-        }
+      if (to.n_splits > 1) {   // this split's fp32 partials
+        float* w = p.ws + partial_at(p.split, to.split, to.tile, BN) + (size_t)c0 * kBM + 32 * quarter + lane;
+        #pragma unroll
+        for (int j = 0; j < 16; ++j) w[j * kBM] = __uint_as_float(v[j]);
       } else {
         // a gate lane finishes columns 0-7, the up lane of the same output columns 8-15
         #pragma unroll
@@ -307,6 +328,7 @@ struct GatherArgs {
   int k[2], k_ld[2];   // k_ld 0: no weak columns
 };
 __global__ void k_gated_gather(const __half* __restrict__ x, int M, int K, const __grid_constant__ GatherArgs a, int* status) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the product's dense steps need none of this
   const int ld = a.k_ld[0] + a.k_ld[1];
   const size_t n = (size_t)M * ld;
   for (size_t e = (size_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (size_t)gridDim.x * blockDim.x) {
@@ -316,46 +338,122 @@ __global__ void k_gated_gather(const __half* __restrict__ x, int M, int K, const
   }
 }
 
-// The split outputs: the planes' partials added in split order, then the epilogue.
-__global__ void k_gated_reduce(const __grid_constant__ GatedGemmParams p, int splits) {
-  const size_t n = p.ws_plane, base = (size_t)p.ws_t0 * p.N;
+// The split tiles: their partials added in split order, then the epilogue.  A warp takes one token
+// of a tile and 32 of its 64 outputs (two runs of 16 MMA rows of either layer).
+__global__ void k_gated_reduce(const __grid_constant__ GatedGemmParams p, int BN) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n_tiles = p.split.tiles - p.split.whole;
+  const size_t n = (size_t)n_tiles * BN * kHalfRows, stride = (size_t)n_tiles * BN * kBM;
   for (size_t e = (size_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (size_t)gridDim.x * blockDim.x) {
-    float gs = p.ws[e], us = p.ws[n + e];
-    for (int z = 1; z < splits; ++z) {
-      gs += p.ws[(size_t)(2 * z) * n + e];
-      us += p.ws[(size_t)(2 * z + 1) * n + e];
+    const int r = (int)(e % kHalfRows), tile = p.split.whole + (int)(e / kHalfRows / BN), t0 = (int)(e / kHalfRows % BN);
+    const int row = (tile % p.rts) * kHalfRows + r, t = (tile / p.rts) * BN + t0;
+    if (row >= p.N || t >= p.M) continue;
+    const float* w = p.ws + partial_at(p.split, 0, tile, BN) + (size_t)t0 * kBM + 32 * (r / 16) + r % 16;
+    float gs = w[0], us = w[16];
+    for (int z = 1; z < p.split.splits; ++z) {
+      gs += w[z * stride];
+      us += w[z * stride + 16];
     }
-    gated_store(p, base + e, gs, us);
+    gated_store(p, (size_t)t * p.N + row, gs, us);
   }
 }
 
 // ---------------------------------------------------------------- input gradient of both layers
-// dx = dg Wg + du Wu: the input-gradient pipeline (see k_igemm_sm100: A = W_hat^T, 128 columns x
-// 128 rows a step, prepared by one warp and formed column by column) run over the gate's rows and
-// then the up layer's into one accumulator.  The weak columns' codes give exactly 0; their
-// products with the fp16 weak blocks are computed before (k_gated_igw) and added in fp32 in the
-// epilogue of the first split, so a column that is weak in one layer and packed in the other is
-// still rounded once.
+// dx = dg Wg + du Wu as dx^T tiles of 128 columns (MMA M, one packed block) x BN tokens (MMA N),
+// the contraction running over the gate's rows and then the up layer's, 128 rows a step, into one
+// accumulator.  The A operand is W_hat^T.  A warp forms it as the decode product forms its
+// fragments: lane (g, t) reads chunk t of row g of an 8-row group, so that each dequantised pair
+// register is an 8 x 8 block of the matrix (rows x columns); movmatrix transposes the block in
+// registers and tcgen05.st 16x128b puts two of them (16 columns) into 16 tensor-memory lanes, two
+// rows packed per 32-bit column.  That is four instructions a pair beside the unpack, and shared
+// memory is read only for the packed words (forming the operand column by column took two 64-bit
+// shared loads and six instructions per pair of rows: 131 KB of shared reads a step, as long as
+// the MMAs).
+// The weak columns' codes give exactly 0; their products with the fp16 weak blocks come from
+// k_gated_igw, running beside this kernel, and are added in fp32 in the epilogue of a tile's first
+// split, so that a column that is weak in one layer and packed in the other is rounded once.
+template <int BITS, int BN, int S>
+constexpr int ig2_smem_bytes() { return S * Smem<BITS, BN>::kStage + 1024 + 1024; }
+
 struct GatedIgMaps {
   CUtensorMap dy[2], p[2], sz[2], dx;
 };
 struct GatedIgParams {
-  float* ws;        // split partials [split][M][K] (NULL: one split, fp16 dx directly)
+  float* ws;        // split partials
   int* status;
   int N, K, M, group;
-  int rsteps;       // 128-row steps per split, of the 2 ceil(N / 128) steps of both layers
+  TileSplit split;  // tile = token tile * (K / 128) + column block; steps: 128 rows, the gate's first
   long long wait_limit;
-  // the weak columns' products, [split][slot][M] per layer
-  const float* wk[2];
+  const float* wk[2];   // the weak columns' products, [row split][slot][M]
   const int32_t* idx[2];
   int k[2], wsplits;
   uint32_t blk[2][kMaxBlocks];   // per column block: first weak slot << 16 | weak-column count
 };
 
-template <int BITS, int BN, int S, int DW>
-__global__ void __launch_bounds__(32 * (3 + DW), 1)
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+// 16 lanes x 16 columns: register 2 i + h of lane 4 r + c holds lane r + 8 h, column 4 i + c
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds_u1(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// The words of a chunk that its pairs 4 Q .. 4 Q + 3 (columns 32 Q .. 32 Q + 31 of the block) use
+template <int BITS, int Q>
+__device__ __forceinline__ void ig_load_words(uint32_t a, uint32_t (&w)[BITS]) {
+  if constexpr (BITS == 4) {
+    const uint2 v = lds_u2(a + 8 * (Q / 2));
+    w[2 * (Q / 2)] = v.x;
+    w[2 * (Q / 2) + 1] = v.y;
+  } else {
+    if (Q != 3) { w[0] = lds_u1(a); w[1] = lds_u1(a + 4); }
+    if (Q >= 2) w[2] = lds_u1(a + 8);
+  }
+}
+
+// One warp's share of a step: columns 32 Q .. 32 Q + 31, RG 8-row groups from shared address `pk`
+// (packed rows) and `sz` ((scale, zero) pairs), to tensor memory at `at` (lane quarter Q).
+template <int BITS, int Q, int RG>
+__device__ __forceinline__ void ig_form(uint32_t pk, uint32_t sz, uint32_t at) {
+  constexpr int NC = BITS == 3 ? 3 : 2;
+  #pragma unroll
+  for (int b = 0; b < RG / 4; ++b) {
+    uint32_t v[2][8];   // [16-column half][16x128b registers of four row groups]
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int rg = 4 * b + i;
+      uint32_t w[BITS];
+      ig_load_words<BITS, Q>(pk + rg * 8 * 16 * BITS, w);
+      const uint32_t z = lds_u1(sz + rg * 32);
+      const uint32_t s2 = __byte_perm(z, z, 0x1010), z2 = __byte_perm(z, z, 0x3232);
+      uint32_t scl[NC], nz[NC];
+      #pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        scl[c] = ((uint32_t)(15 - class_off<BITS>(c)) << 10) * 0x00010001u;                                // 2^-o
+        nz[c] = h2_sub((0x8000u | ((uint32_t)(25 - class_off<BITS>(c)) << 10)) * 0x00010001u, z2);   // -(2^(10 - o) + z)
+      }
+      #pragma unroll
+      for (int p = 0; p < 4; ++p)
+        v[p >> 1][2 * i + (p & 1)] = movmatrix(dequant_pair<BITS>(w, 4 * Q + p, s2, scl, nz));
+    }
+    #pragma unroll
+    for (int h = 0; h < 2; ++h) tmem_st_16x128b_x4(at + ((uint32_t)(16 * h) << 16) + 16 * b, v[h]);
+  }
+}
+
+template <int BITS, int BN, int S, int GR>
+__global__ void __launch_bounds__(32 * (2 + kDW), 1)
 k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ GatedIgParams p) {
-  using L = IgSmem<BITS, BN>;
+  using L = Smem<BITS, BN>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * L::kStage);
@@ -363,23 +461,22 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
   uint64_t* empty = bars + S;       // [S] MMAs of the stage done
   uint64_t* afull = bars + 2 * S;   // [S] A tile written to tensor memory
   uint64_t* accf = bars + 3 * S;    // accumulator complete
-  uint64_t* pfull = bars + 3 * S + 1;   // [S] prep warp's words written
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * S + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.x;             // column block (128 columns)
-  const int m0 = blockIdx.y * BN;       // first token
+  const int Kb = p.K / kStepCodes;
   const int nR = (p.N + 127) / 128;     // row steps of one layer
-  const int rb0 = blockIdx.z * p.rsteps;                     // first step of this split
-  const int nK = max(0, min(p.rsteps, 2 * nR - rb0));
+  const TileOf to = tile_of(p.split, blockIdx.x, 2 * nR);
+  const int b = to.tile % Kb;           // column block (128 columns)
+  const int m0 = (to.tile / Kb) * BN;   // first token
+  const int nK = to.steps;
   const int grp = (b * kStepCodes) / p.group;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&afull[s], 32 * DW);
-      mbar_init(&pfull[s], 32);
+      mbar_init(&afull[s], 32 * kDW / GR);
     }
     mbar_init(accf, 1);
     fence_mbar_init();
@@ -391,6 +488,7 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
     }
   }
   if (warp == 1) tmem_alloc(tmem_slot, tmem_cols<BN, S>());
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -406,8 +504,8 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
         if (u > 0) ok = mbar_wait(&empty[s], (u - 1) & 1, p.status, p.wait_limit);
         if (!ok) break;
         unsigned char* st = smem + s * L::kStage;
-        const int l = rb0 + i >= nR, rb = rb0 + i - (l ? nR : 0);
-        mbar_arrive_expect_tx(&full[s], L::kTma);
+        const int l = to.first + i >= nR, rb = to.first + i - (l ? nR : 0);
+        mbar_arrive_expect_tx(&full[s], L::kX + L::kP + L::kSZ);
         tma_load_3d(st + L::kX, &maps.p[l], &full[s], 0, b, rb * 8);
         tma_load_3d(st + L::kX + L::kP, &maps.sz[l], &full[s], 0, grp, rb * 8);
         tma_load_2d(st, &maps.dy[l], &full[s], rb * 128, m0);
@@ -438,89 +536,107 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
       }
       mma_commit(accf);
     }
-  } else if (warp == 2 + DW) {
-    // ---------------- prep warp ----------------
-    bool ok = true;
-    for (int i = 0; i < nK && ok; ++i) {
-      const int s = i % S, u = i / S;
-      ok = mbar_wait(&full[s], u & 1, p.status, p.wait_limit);
-      if (!ok) break;
-      const uint32_t st = smem_u32(smem) + s * L::kStage;   // shared address of the stage
-      ig_prep_step<BITS, BN>(st, lane);
-      __syncwarp();
-      mbar_arrive(&pfull[s]);
-    }
   } else {
     // ---------------- A operand: W_hat^T ----------------
-    constexpr int NSL = DW / 4, RP = 64 / NSL;
-    const int quarter = warp & 3, jh = (warp - 2) >> 2;
-    const int j = 32 * quarter + lane;             // column of the block
-    const IgColumn<BITS, BN> cj(j);
+    // group grp of the steps; within it lane quarter = warp % 4 (32 columns) and row slab jh
+    constexpr int NSL = kDW / GR / 4, RG = 16 / NSL;   // 8-row groups of a warp's slab
+    const int quarter = warp & 3, aw = warp - 2, gr = aw / (kDW / GR), jh = (aw % (kDW / GR)) >> 2;
+    const int g = lane >> 2, t = lane & 3;
     const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
+    const uint32_t sm = smem_u32(smem);
     bool ok = true;
-    for (int i = 0; i < nK && ok; ++i) {
+    for (int i = gr; i < nK && ok; i += GR) {
       const int s = i % S, u = i / S;
-      ok = mbar_wait(&pfull[s], u & 1, p.status, p.wait_limit);   // (implies the TMA landed)
+      ok = __all_sync(0xffffffffu, mbar_wait(&full[s], u & 1, p.status, p.wait_limit));   // (also: the stage's previous MMAs are done)
       if (!ok) break;
       tc_fence_after();
-      const uint32_t st = smem_u32(smem) + s * L::kStage;   // shared address of the stage
-      uint32_t d[RP];
-      cj.operand<RP>(st, RP * jh, d);
-      const uint32_t at = tmem + lane_base + BN + 64 * s + RP * jh;
-      #pragma unroll
-      for (int c = 0; c < RP / 16; ++c)
-        tmem_st16(at + 16 * c, *reinterpret_cast<const uint32_t(*)[16]>(d + 16 * c));
+      const uint32_t st = sm + s * L::kStage;
+      const uint32_t pk = st + L::kX + (8 * RG * jh + g) * 16 * BITS + t * 4 * BITS;
+      const uint32_t sz = st + L::kX + L::kP + (8 * RG * jh + g) * 4;
+      const uint32_t at = tmem + lane_base + BN + 64 * s + 4 * RG * jh;
+      switch (quarter) {
+        case 0: ig_form<BITS, 0, RG>(pk, sz, at); break;
+        case 1: ig_form<BITS, 1, RG>(pk, sz, at); break;
+        case 2: ig_form<BITS, 2, RG>(pk, sz, at); break;
+        default: ig_form<BITS, 3, RG>(pk, sz, at); break;
+      }
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&afull[s]);
     }
 
     // ---------------- epilogue ----------------
-    // this column's weak slot in each layer (-1: packed there); added by the first split
-    const int col = b * kStepCodes + j;
-    int slot[2] = {-1, -1};
-    if (blockIdx.z == 0) {
+    // One split: the fp16 tile goes through shared memory ([BN tokens][128 columns], the stages are
+    // idle once the accumulator is complete) and out with one TMA store; several: fp32 partials.
+    bool acc_ok = __all_sync(0xffffffffu, mbar_wait(accf, 0, p.status, p.wait_limit)) && ok;
+    tc_fence_after();
+    const int j = 32 * quarter + lane, col = b * kStepCodes + j;   // this thread's column
+    __half* s_out = reinterpret_cast<__half*>(smem);
+    // the weak columns of this block in either layer: their products' row splits added in order
+    // into shared memory (behind the output tile; those that do not fit are added from global)
+    constexpr int kWkCap = (S * L::kStage - BN * kStepCodes * 2) / (BN * 4);
+    int slot[2] = {-1, -1}, at_wk[2] = {0, 0}, n_weak = 0;   // this column's weak slot, and its place
+    float* s_wk = reinterpret_cast<float*>(smem + BN * kStepCodes * 2);   // [weak column][BN]
+    if (to.split == 0) {
       #pragma unroll
       for (int l = 0; l < 2; ++l) {
-        if (p.k[l] == 0) continue;
-        const int first = (int)(p.blk[l][b] >> 16), cnt = (int)(p.blk[l][b] & 0xFFFFu);
-        for (int t = first; t < first + cnt; ++t)
-          if (in_range(t, p.k[l], p.status) && p.idx[l][t] == col) slot[l] = t;
+        const int first = p.k[l] > 0 ? (int)(p.blk[l][b] >> 16) : 0, cnt = p.k[l] > 0 ? (int)(p.blk[l][b] & 0xFFFFu) : 0;
+        if (n_weak == 0 && cnt > 0) asm volatile("griddepcontrol.wait;" ::: "memory");   // k_gated_igw's results
+        for (int c = 0; c < cnt; ++c)
+          if (in_range(first + c, p.k[l], p.status) && p.idx[l][first + c] == col) { slot[l] = first + c; at_wk[l] = n_weak + c; }
+        const size_t plane = (size_t)p.k[l] * p.M;
+        for (int e = (int)threadIdx.x - 64; e < min(cnt, kWkCap - n_weak) * BN && acc_ok; e += 32 * kDW) {
+          const int c = e / BN, tk = e - c * BN;
+          float v = 0.f;
+          if (m0 + tk < p.M) {
+            const float* wk = p.wk[l] + (size_t)(first + c) * p.M + m0 + tk;
+            #pragma unroll 8
+            for (int z = 0; z < p.wsplits; ++z) v += __ldcg(wk + z * plane);
+          }
+          s_wk[(n_weak + c) * BN + tk] = v;
+        }
+        n_weak += cnt;
       }
+      named_bar_sync(1, 32 * kDW);
     }
-    const bool acc_ok = __all_sync(0xffffffffu, mbar_wait(accf, 0, p.status, p.wait_limit) && ok);
-    tc_fence_after();
-    __half* s_out = reinterpret_cast<__half*>(smem);
+    constexpr int kCols = BN / (kDW / 4);   // accumulator columns (tokens) of this warp
+    const int col0 = (aw >> 2) * kCols;
     #pragma unroll 1
-    for (int c0 = jh * (BN / NSL); c0 < (jh + 1) * (BN / NSL); c0 += 16) {
+    for (int c0 = col0; c0 < col0 + kCols; c0 += 16) {
       uint32_t v[16];
       tmem_ld16(tmem + lane_base + (uint32_t)c0, v);
       tmem_ld_wait();
       #pragma unroll
       for (int l = 0; l < 2; ++l)
-        if (slot[l] >= 0)
-          for (int z = 0; z < p.wsplits; ++z) {
-            const float* wk = p.wk[l] + ((size_t)z * p.k[l] + slot[l]) * p.M + m0 + c0;
+        if (slot[l] >= 0) {
+          if (at_wk[l] < kWkCap) {
             #pragma unroll
-            for (int t = 0; t < 16; ++t)
-              if (m0 + c0 + t < p.M) v[t] = __float_as_uint(__uint_as_float(v[t]) + wk[t]);
+            for (int tk = 0; tk < 16; ++tk) v[tk] = __float_as_uint(__uint_as_float(v[tk]) + s_wk[at_wk[l] * BN + c0 + tk]);
+          } else {
+            #pragma unroll
+            for (int tk = 0; tk < 16; ++tk) {
+              float w = 0.f;
+              for (int z = 0; z < p.wsplits && m0 + c0 + tk < p.M; ++z)
+                w += __ldcg(p.wk[l] + ((size_t)z * p.k[l] + slot[l]) * p.M + m0 + c0 + tk);
+              v[tk] = __float_as_uint(__uint_as_float(v[tk]) + w);
+            }
           }
-      if (p.ws) {
+        }
+      if (to.n_splits > 1) {
         if (acc_ok) {
-          float* w = p.ws + (size_t)blockIdx.z * p.M * p.K;
+          float* w = p.ws + partial_at(p.split, to.split, to.tile, BN) + (size_t)c0 * kBM + j;
           #pragma unroll
-          for (int t = 0; t < 16; ++t)
-            if (m0 + c0 + t < p.M) w[(size_t)(m0 + c0 + t) * p.K + col] = __uint_as_float(v[t]);
+          for (int tk = 0; tk < 16; ++tk) w[tk * kBM] = __uint_as_float(v[tk]);
         }
       } else {
         #pragma unroll
-        for (int t = 0; t < 16; ++t)
-          sts_u16(smem_u32(s_out) + 2 * ((c0 + t) * kStepCodes + j), __half_as_ushort(__float2half_rn(__uint_as_float(v[t]))));
+        for (int tk = 0; tk < 16; ++tk)
+          sts_u16(smem_u32(s_out) + 2 * ((c0 + tk) * kStepCodes + j), __half_as_ushort(__float2half_rn(__uint_as_float(v[tk]))));
       }
     }
-    if (!p.ws) {
+    if (to.n_splits == 1) {
       fence_proxy_async_smem();          // the tile, written by the generic proxy, to the TMA
-      named_bar_sync(1, 32 * DW);        // every A thread's part of the tile is written
+      named_bar_sync(1, 32 * kDW);       // every A thread's part of the tile is written
       if (warp == 2 && lane == 0 && acc_ok) {
         tma_store_2d(&maps.dx, s_out, b * kStepCodes, m0);
         bulk_commit();
@@ -538,27 +654,32 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
   }
 }
 
-// dx = fp16_rn(the splits' partials added in split order); n = M K outputs (a multiple of 128)
-__global__ void k_gated_ig_reduce(const float* __restrict__ ws, int splits, size_t n, __half* __restrict__ dx) {
+// dx of the split tiles = fp16_rn(their partials added in split order)
+__global__ void k_gated_ig_reduce(const __grid_constant__ GatedIgParams p, int BN, __half* __restrict__ dx) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n_tiles = p.split.tiles - p.split.whole, Kb = p.K / kStepCodes;
+  const size_t n = (size_t)n_tiles * BN * kBM;
   for (size_t e = 4 * ((size_t)blockIdx.x * blockDim.x + threadIdx.x); e < n; e += 4 * (size_t)gridDim.x * blockDim.x) {
-    float4 v = *reinterpret_cast<const float4*>(ws + e);
-    for (int z = 1; z < splits; ++z) {
-      const float4 w = *reinterpret_cast<const float4*>(ws + (size_t)z * n + e);
+    const int c = (int)(e % kBM), t0 = (int)(e / kBM % BN), tile = p.split.whole + (int)(e / kBM / BN);
+    const int t = (tile / Kb) * BN + t0;
+    if (t >= p.M) continue;
+    float4 v = *reinterpret_cast<const float4*>(p.ws + e);
+    for (int z = 1; z < p.split.splits; ++z) {
+      const float4 w = *reinterpret_cast<const float4*>(p.ws + (size_t)z * n + e);
       v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
     }
-    __half2* o = reinterpret_cast<__half2*>(dx + e);
+    __half2* o = reinterpret_cast<__half2*>(dx + (size_t)t * p.K + (tile % Kb) * kStepCodes + c);
     o[0] = __floats2half2_rn(v.x, v.y);
     o[1] = __floats2half2_rn(v.z, v.w);
   }
 }
 
-// The weak columns' products of both layers, wk[l][split][slot][m] = sum_i dy_l[m][i] w_weak_l[i][slot]
-// over a split of the rows (mma.sync m16n8k16: rows = tokens, K = weight rows, columns = slots).
-// A CTA of 4 warps computes 64 tokens x 32 slots of one layer, 32 rows at a time through a 4-stage
-// cp.async ring.  (As k_igw_mma, but to fp32 and token-contiguous: the input-gradient epilogue
-// reads a slot's tokens.)
-constexpr int kIwTok = 64, kIwCols = 32, kIwRows = 32, kIwThreads = 128, kIwStages = 4;
-constexpr int kIwDyLd = kIwRows + 8, kIwWLd = kIwCols + 8;   // padded row strides (halves)
+// The weak columns' products of both layers, wk[l][row split][slot][m] = sum_i dy_l[m][i]
+// w_weak_l[i][slot] (mma.sync m16n8k16: rows = tokens, K = weight rows, columns = slots).  A CTA of
+// 4 warps computes 64 tokens x CT slots of one layer over one split of the rows, 32 rows at a time
+// through a 4-stage cp.async ring.  Bound by reading the gradients, once per CT slots.
+constexpr int kIwTok = 64, kIwRows = 32, kIwThreads = 128, kIwStages = 4, kIwMaxSplits = 8;
+constexpr int kIwDyLd = kIwRows + 8;   // padded row stride (halves)
 
 struct GatedIgwArgs {
   const __half* dy[2];
@@ -567,15 +688,17 @@ struct GatedIgwArgs {
   int k[2], k_ld[2], ctiles0;   // slot tiles of the gate layer (blockIdx.y below it)
   int N, ldy, M, per;           // per: rows per split, a multiple of 32
 };
+template <int CT>
 __global__ void __launch_bounds__(kIwThreads) k_gated_igw(const __grid_constant__ GatedIgwArgs a) {
   __shared__ __align__(128) __half s_dy[kIwStages][kIwTok][kIwDyLd];
-  __shared__ __align__(128) __half s_w[kIwStages][kIwRows][kIwWLd];
+  __shared__ __align__(128) __half s_w[kIwStages][kIwRows][CT + 8];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the packed product runs beside this
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int l = (int)blockIdx.y >= a.ctiles0;
   const __half* __restrict__ dy = a.dy[l];
   const __half* __restrict__ w = a.w[l];
   const int k = a.k[l], k_ld = a.k_ld[l];
-  const int mb = blockIdx.x * kIwTok, t0 = ((int)blockIdx.y - (l ? a.ctiles0 : 0)) * kIwCols;
+  const int mb = blockIdx.x * kIwTok, t0 = ((int)blockIdx.y - (l ? a.ctiles0 : 0)) * CT;
   const int i_lo = blockIdx.z * a.per, i_hi = min(a.N, i_lo + a.per);
   const int nchunk = max(0, (i_hi - i_lo + kIwRows - 1) / kIwRows);
   auto load = [&](int c, int st) {   // rows i_lo + 32 c .. of this split into stage st
@@ -587,15 +710,16 @@ __global__ void __launch_bounds__(kIwThreads) k_gated_igw(const __grid_constant_
       const bool ok = mm < a.M && row < i_hi;
       cp_async16(&s_dy[st][m][pc * 8], dy + (ok ? (size_t)mm * a.ldy + row : 0), ok);
     }
-    {                                // weak block: 32 rows x 4 pieces of 8 slots
-      const int r = tid >> 2, pc = tid & 3, row = ib + r, col = t0 + pc * 8;
+    #pragma unroll
+    for (int u = 0; u < CT / 32; ++u) {   // weak block: 32 rows x CT / 8 pieces of 8 slots
+      const int e = tid + u * kIwThreads, r = e / (CT / 8), pc = e % (CT / 8), row = ib + r, col = t0 + pc * 8;
       const bool ok = row < i_hi && col < k_ld;
       cp_async16(&s_w[st][r][pc * 8], w + (ok ? (size_t)row * k_ld + col : 0), ok);
     }
   };
-  float d[4][4];
+  float d[CT / 8][4];
   #pragma unroll
-  for (int n = 0; n < 4; ++n)
+  for (int n = 0; n < CT / 8; ++n)
     #pragma unroll
     for (int i = 0; i < 4; ++i) d[n][i] = 0.f;
   #pragma unroll
@@ -616,7 +740,7 @@ __global__ void __launch_bounds__(kIwThreads) k_gated_igw(const __grid_constant_
       uint32_t f[4];   // tokens 16 warp + 0..15 x rows mk..mk+15
       ldsm_x4(f, &s_dy[st][warp * 16 + (q & 1) * 8 + r8][mk + (q >> 1) * 8]);
       #pragma unroll
-      for (int nh = 0; nh < 2; ++nh) {
+      for (int nh = 0; nh < CT / 16; ++nh) {
         uint32_t bb[4];   // rows mk..mk+15 x slots 16 nh..16 nh+15, read transposed (two n8 tiles)
         ldsm_x4_t(bb, &s_w[st][mk + (q & 1) * 8 + r8][nh * 16 + (q >> 1) * 8]);
         mma_16816(d[2 * nh], f, bb[0], bb[1]);
@@ -627,7 +751,7 @@ __global__ void __launch_bounds__(kIwThreads) k_gated_igw(const __grid_constant_
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   const int g = lane >> 2, c4 = lane & 3;
   #pragma unroll
-  for (int n = 0; n < 4; ++n)
+  for (int n = 0; n < CT / 8; ++n)
     #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int m = mb + warp * 16 + g + 8 * (i >> 1), t = t0 + n * 8 + 2 * c4 + (i & 1);
@@ -654,19 +778,58 @@ unsigned blocks_for(size_t n, int threads, unsigned most) {
   return (unsigned)std::max<size_t>(1, std::min<size_t>((n + threads - 1) / threads, most));
 }
 
+// Tokens of a tile.  A tile's time is set by forming the A operand up to about 128 tokens and by
+// the MMAs above, so one wide tile beats two narrower ones.
+int gated_tile_tokens(int M) { return M <= 64 ? 64 : M <= 128 ? 128 : 256; }
+
+// The split of T tiles of `steps` steps over P SMs (see TileSplit): at least 4 steps a split, and
+// only where the saved time, in units of a step (about 0.3 us for 64 tokens to 0.65 us for 256),
+// exceeds the partials' way through L2 and the reduction's launch (about 4 us).
+TileSplit plan_split(long long T, int steps, int BN, int P) {
+  TileSplit s = {(int)T, (int)T, 1, steps};
+  const int rem = (int)(T % P);
+  if (rem == 0) return s;
+  int n = std::min(P / rem, steps / 4);
+  if (n < 2) return s;
+  const int per = (steps + n - 1) / n;
+  n = (steps + per - 1) / per;
+  const double step_us = BN == 64 ? 0.3 : BN == 128 ? 0.4 : 0.65;
+  const double cost_us = 4.0 + 2.0 * n * rem * BN * kBM * sizeof(float) / 5e6;
+  if ((steps - per) * step_us <= cost_us) return s;
+  s.whole = (int)(T - rem);
+  s.splits = n;
+  s.steps = per;
+  return s;
+}
+size_t partial_bytes(const TileSplit& s, int BN) {
+  return s.splits > 1 ? up256((size_t)s.splits * (s.tiles - s.whole) * BN * kBM * sizeof(float)) : 0;
+}
+
+cudaError_t launch_pdl(void* kern, dim3 grid, int threads, size_t smem, bool pdl, cudaStream_t s, void** args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelExC(&cfg, kern, args);
+}
+
 // workspace of one forward / backward product: both layers' weak activations, then the split partials
 struct FwdPlan {
-  GemmPlan g;
-  int t0, nsp;              // first token with split partials, splits there
+  int BN, rts;
+  TileSplit split;
   size_t xw[2], ws, total;  // byte offsets
 };
 FwdPlan fwd_plan(const Layer& gate, const Layer& up, int M) {
   FwdPlan f;
-  const int RT = (gate.N + kHalfRows - 1) / kHalfRows;
-  f.g = gemm_plan(RT * kBM, gate.K, M, layer_sm_count(gate.device));
-  const int BN = f.g.tile_tokens, TT = (M + BN - 1) / BN;
-  f.t0 = f.g.tail_sp > 1 ? (TT - f.g.tail_tt) * BN : 0;
-  f.nsp = f.g.tail_sp > 1 ? f.g.tail_sp : f.g.splits;
+  f.BN = gated_tile_tokens(M);
+  f.rts = (gate.N + kHalfRows - 1) / kHalfRows;
+  f.split = plan_split((long long)f.rts * ((M + f.BN - 1) / f.BN), gate.K / kStepCodes, f.BN, layer_sm_count(gate.device));
   size_t at = 0;
   const Layer* L[2] = {&gate, &up};
   for (int l = 0; l < 2; ++l) {
@@ -674,12 +837,11 @@ FwdPlan fwd_plan(const Layer& gate, const Layer& up, int M) {
     if (L[l]->k > 0) at += up256((size_t)M * L[l]->k_ld * sizeof(__half));
   }
   f.ws = at;
-  if (f.nsp > 1) at += up256((size_t)f.nsp * 2 * (M - f.t0) * gate.N * sizeof(float));
-  f.total = at;
+  f.total = at + partial_bytes(f.split, f.BN);
   return f;
 }
 
-template <int BITS, int BN, int S, int DW>
+template <int BITS, int BN, int S, int GR>
 owq_status_t run_gemm(const Layer& gate, const Layer& up, int act, const __half* x, const __half* dh, __half* out0, __half* out1,
                       int M, const FwdPlan& f, unsigned char* ws, long long wait_limit, bool skip_arrive, cudaStream_t s) {
   const Layer* L[2] = {&gate, &up};
@@ -713,19 +875,10 @@ owq_status_t run_gemm(const Layer& gate, const Layer& up, int act, const __half*
   prm.N = gate.N; prm.K = gate.K; prm.M = M; prm.G = gate.G; prm.act = act;
   prm.wait_limit = wait_limit; prm.skip_arrive = skip_arrive ? 1 : 0;
   prm.nw = (std::max(prm.k_ld[0], prm.k_ld[1]) + 63) / 64;
-  const int RT = (gate.N + kHalfRows - 1) / kHalfRows, TT = (M + BN - 1) / BN;
-  prm.ksteps = f.g.ksteps;
-  prm.tail_y0 = TT - f.g.tail_tt;
-  prm.tail_sp = f.g.tail_sp;
-  prm.tail_ksteps = f.g.tail_ksteps;
+  prm.rts = f.rts;
+  prm.split = f.split;
   prm.ws = reinterpret_cast<float*>(ws + f.ws);
-  prm.ws_t0 = f.t0;
-  prm.ws_plane = (size_t)(M - f.t0) * gate.N;
-  auto kern = k_gated_gemm<BITS, BN, S, DW, false>;
-  if (f.g.tail_sp > 1) {
-    if constexpr (BN > 64) kern = k_gated_gemm<BITS, BN, S, DW, true>;
-    else return OWQ_ERR_CUDA;   // never planned: a tail needs two token tiles
-  }
+  auto kern = k_gated_gemm<BITS, BN, S, GR>;
   constexpr int smem = smem_bytes<BITS, BN, S>();
   static_assert(smem <= 232448, "shared memory budget");
   static_assert(BN + 64 * S <= (int)tmem_cols<BN, S>(), "tensor memory: accumulator + A stages");
@@ -739,12 +892,20 @@ owq_status_t run_gemm(const Layer& gate, const Layer& up, int act, const __half*
     k_gated_gather<<<blocks_for((size_t)M * ld, 256, 2048), 256, 0, s>>>(x, M, gate.K, ga, prm.status);
     if (cudaGetLastError() != cudaSuccess) return OWQ_ERR_CUDA;
   }
-  const dim3 grid(RT, prm.tail_y0 + f.g.tail_tt * f.g.tail_sp, f.g.splits);
-  kern<<<grid, 32 * (2 + DW), smem, s>>>(maps, prm);
-  if (cudaGetLastError() != cudaSuccess) return OWQ_ERR_CUDA;
-  if (f.nsp > 1) {
-    k_gated_reduce<<<blocks_for(prm.ws_plane, 256, 4096), 256, 0, s>>>(prm, f.nsp);
-    if (cudaGetLastError() != cudaSuccess) return OWQ_ERR_CUDA;
+  // beside the gather: only the weak steps wait for it
+  void* args[] = {&maps, &prm};
+  if (launch_pdl((void*)kern, dim3(f.split.ctas()), 32 * (2 + kDW), smem, ld > 0, s, args) != cudaSuccess) {
+    cudaGetLastError();
+    return OWQ_ERR_CUDA;
+  }
+  if (f.split.splits > 1) {
+    int bn = BN;
+    void* rargs[] = {&prm, &bn};
+    const size_t n = (size_t)(f.split.tiles - f.split.whole) * BN * kHalfRows;
+    if (launch_pdl((void*)k_gated_reduce, dim3(blocks_for(n, 256, 4096)), 256, 0, true, s, rargs) != cudaSuccess) {
+      cudaGetLastError();
+      return OWQ_ERR_CUDA;
+    }
   }
   return OWQ_OK;
 }
@@ -752,39 +913,37 @@ owq_status_t run_gemm(const Layer& gate, const Layer& up, int act, const __half*
 template <int BITS>
 owq_status_t dispatch_gemm(const Layer& gate, const Layer& up, int act, const __half* x, const __half* dh, __half* out0,
                            __half* out1, int M, const FwdPlan& f, unsigned char* ws, long long wl, bool skip, cudaStream_t s) {
-  switch (f.g.tile_tokens) {
-    case 64: return run_gemm<BITS, 64, 6, 8>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
-    case 128: return run_gemm<BITS, 128, 4, 8>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
-    default: return run_gemm<BITS, 256, 3, 16>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
+  switch (f.BN) {
+    case 64: return run_gemm<BITS, 64, 6, 2>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
+    case 128: return run_gemm<BITS, 128, 4, 2>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
+    default: return run_gemm<BITS, 256, 3, OWQ_GR256>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
   }
 }
 
 // workspace of one input gradient: padded gradients (N % 8 != 0), the weak products, the split partials
 struct IgPlan {
-  int BN, splits, rsteps;   // row splits over both layers' 128-row steps
-  int ldy, wsplits, wper;
+  int BN;
+  TileSplit split;
+  int ldy, ct, wsplits, wper;   // weak products: slots of a tile, row splits, rows of a split
   size_t pad[2], wk[2], ws, total;
 };
 IgPlan ig_plan(const Layer& gate, const Layer& up, int M) {
   IgPlan f;
   const int sms = layer_sm_count(gate.device);
-  const int Kb = gate.K / kStepCodes, nR = 2 * ((gate.N + 127) / 128);
-  f.BN = gemm_tile_tokens(M);
-  const long long tiles = (long long)Kb * ((M + f.BN - 1) / f.BN);
-  // fewer tiles than SMs: the rows split over CTAs, at least 4 steps each
-  f.splits = tiles < sms ? (int)std::max<long long>(1, std::min<long long>(sms / tiles, nR / 4)) : 1;
-  f.rsteps = (nR + f.splits - 1) / f.splits;
-  f.splits = (nR + f.rsteps - 1) / f.rsteps;
+  f.BN = gated_tile_tokens(M);
+  f.split = plan_split((long long)(gate.K / kStepCodes) * ((M + f.BN - 1) / f.BN), 2 * ((gate.N + 127) / 128), f.BN, sms);
   f.ldy = (gate.N + 7) & ~7;
   size_t at = 0;
   for (int l = 0; l < 2; ++l) {
     f.pad[l] = at;
     if (gate.N % 8) at += up256((size_t)M * f.ldy * sizeof(__half));
   }
-  // weak products: about two CTAs per SM, at least 4 chunks of 32 rows each
-  const int R = (M + kIwTok - 1) / kIwTok, C = (gate.k + kIwCols - 1) / kIwCols + (up.k + kIwCols - 1) / kIwCols;
+  // weak products: about two CTAs per SM; at least 4 chunks of 32 rows and at most kIwMaxSplits
+  // splits (the input gradient's epilogue adds them)
+  f.ct = std::max(gate.k, up.k) > 32 ? 64 : 32;
+  const int R = (M + kIwTok - 1) / kIwTok, C = (gate.k + f.ct - 1) / f.ct + (up.k + f.ct - 1) / f.ct;
   const int nch = (gate.N + kIwRows - 1) / kIwRows;
-  f.wsplits = C > 0 ? std::max(1, std::min((2 * sms + R * C - 1) / (R * C), nch / 4)) : 1;
+  f.wsplits = C > 0 ? std::max(1, std::min({(2 * sms + R * C - 1) / (R * C), nch / 4, kIwMaxSplits})) : 1;
   f.wper = (nch + f.wsplits - 1) / f.wsplits;
   f.wsplits = (nch + f.wper - 1) / f.wper;
   f.wper *= kIwRows;
@@ -793,12 +952,11 @@ IgPlan ig_plan(const Layer& gate, const Layer& up, int M) {
   f.wk[1] = at;
   at += up256((size_t)f.wsplits * up.k * M * sizeof(float));
   f.ws = at;
-  if (f.splits > 1) at += up256((size_t)f.splits * M * gate.K * sizeof(float));
-  f.total = at;
+  f.total = at + partial_bytes(f.split, f.BN);
   return f;
 }
 
-template <int BITS, int BN, int S, int DW>
+template <int BITS, int BN, int S, int GR>
 owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const __half* du, __half* dx, int M, const IgPlan& f,
                     unsigned char* ws, long long wait_limit, cudaStream_t s) {
   const Layer* L[2] = {&gate, &up};
@@ -834,32 +992,42 @@ owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const 
   prm.status = device_status_ptr();
   if (!prm.status) return OWQ_ERR_CUDA;
   prm.N = gate.N; prm.K = gate.K; prm.M = M; prm.group = gate.group;
-  prm.rsteps = f.rsteps;
+  prm.split = f.split;
   prm.wait_limit = wait_limit;
   prm.wsplits = f.wsplits;
-  prm.ws = f.splits > 1 ? reinterpret_cast<float*>(ws + f.ws) : nullptr;
-  wa.ctiles0 = (gate.k + kIwCols - 1) / kIwCols;
+  prm.ws = reinterpret_cast<float*>(ws + f.ws);
+  wa.ctiles0 = (gate.k + f.ct - 1) / f.ct;
   wa.N = gate.N; wa.ldy = f.ldy; wa.M = M; wa.per = f.wper;
-  const int C = wa.ctiles0 + (up.k + kIwCols - 1) / kIwCols;
-  if (C > 0) {
-    k_gated_igw<<<dim3((M + kIwTok - 1) / kIwTok, C, f.wsplits), kIwThreads, 0, s>>>(wa);
-    if (cudaGetLastError() != cudaSuccess) return OWQ_ERR_CUDA;
-  }
-  auto kern = k_gated_igemm<BITS, BN, S, DW>;
-  constexpr int smem = ig_smem_bytes<BITS, BN, S>();
+  const int C = wa.ctiles0 + (up.k + f.ct - 1) / f.ct;
+  auto kern = k_gated_igemm<BITS, BN, S, GR>;
+  constexpr int smem = ig2_smem_bytes<BITS, BN, S>();
   static_assert(smem <= 232448, "shared memory budget");
   static_assert((232448 / smem) * tmem_cols<BN, S>() <= 512, "tensor memory per SM");
-  static_assert(BN * kStepCodes * 2 <= IgSmem<BITS, BN>::kStage, "output tile in the first stage");
+  static_assert(BN * kStepCodes * 2 <= Smem<BITS, BN>::kStage, "output tile in the first stage");
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
     cudaGetLastError();
     return OWQ_ERR_CUDA;
   }
-  kern<<<dim3(Kb, (M + BN - 1) / BN, f.splits), 32 * (3 + DW), smem, s>>>(maps, prm);
-  if (cudaGetLastError() != cudaSuccess) return OWQ_ERR_CUDA;
-  if (f.splits > 1) {
-    const size_t n = (size_t)M * gate.K;
-    k_gated_ig_reduce<<<blocks_for(n / 4, 256, 4096), 256, 0, s>>>(prm.ws, f.splits, n, dx);
+  if (C > 0) {
+    const dim3 grid((M + kIwTok - 1) / kIwTok, C, f.wsplits);
+    if (f.ct == 64) k_gated_igw<64><<<grid, kIwThreads, 0, s>>>(wa);
+    else k_gated_igw<32><<<grid, kIwThreads, 0, s>>>(wa);
     if (cudaGetLastError() != cudaSuccess) return OWQ_ERR_CUDA;
+  }
+  // beside the weak products: only the epilogues of blocks with weak columns wait for them
+  void* args[] = {&maps, &prm};
+  if (launch_pdl((void*)kern, dim3(f.split.ctas()), 32 * (2 + kDW), smem, C > 0, s, args) != cudaSuccess) {
+    cudaGetLastError();
+    return OWQ_ERR_CUDA;
+  }
+  if (f.split.splits > 1) {
+    int bn = BN;
+    void* rargs[] = {&prm, &bn, &dx};
+    const size_t n = (size_t)(f.split.tiles - f.split.whole) * BN * kBM;
+    if (launch_pdl((void*)k_gated_ig_reduce, dim3(blocks_for(n / 4, 256, 4096)), 256, 0, true, s, rargs) != cudaSuccess) {
+      cudaGetLastError();
+      return OWQ_ERR_CUDA;
+    }
   }
   return OWQ_OK;
 }
@@ -868,9 +1036,9 @@ template <int BITS>
 owq_status_t dispatch_ig(const Layer& gate, const Layer& up, const __half* dg, const __half* du, __half* dx, int M, const IgPlan& f,
                          unsigned char* ws, long long wl, cudaStream_t s) {
   switch (f.BN) {
-    case 64: return run_ig<BITS, 64, 6, 8>(gate, up, dg, du, dx, M, f, ws, wl, s);
-    case 128: return run_ig<BITS, 128, 4, 8>(gate, up, dg, du, dx, M, f, ws, wl, s);
-    default: return run_ig<BITS, 256, 3, 16>(gate, up, dg, du, dx, M, f, ws, wl, s);
+    case 64: return run_ig<BITS, 64, 6, 2>(gate, up, dg, du, dx, M, f, ws, wl, s);
+    case 128: return run_ig<BITS, 128, 4, 2>(gate, up, dg, du, dx, M, f, ws, wl, s);
+    default: return run_ig<BITS, 256, 3, OWQ_GR256>(gate, up, dg, du, dx, M, f, ws, wl, s);
   }
 }
 
