@@ -16,6 +16,7 @@
 #include <type_traits>
 
 #include "owq_act.cuh"
+#include "owq_dequant.cuh"
 #include "owq_gemm_common.cuh"
 #include "owq_mma.cuh"
 
@@ -26,25 +27,41 @@ using namespace sm100;
 
 constexpr int kHalfRows = kBM / 2;     // output rows of a tile: 64 of each layer
 constexpr int kDW = 16;                // A-operand warps
-#ifndef OWQ_GR256
-#define OWQ_GR256 2
-#endif
+constexpr int kGR = 2;                 // groups of them, on alternate steps
+constexpr int kS2 = 4;                 // A stages in tensor memory
+constexpr uint32_t kTmemCols = 512;    // accumulator (up to 256 columns) and kS2 x 64
 
-// How the tiles of a product become CTAs: `whole` tiles take one CTA each; each of the others is
-// split `splits` ways over its steps (`steps` a split).  CTAs are dispatched in index order, so the
-// split tiles run last.  The plain order would leave the last wave short: T tiles on P SMs take
-// ceil(T / P) tile times, with the last T mod P of them split over the idle SMs about T / P.
+// One ring stage of a CTA: half of the step's tokens (two 128B-swizzled boxes of 64 columns), the
+// packed block of its 128 rows and their (scale, zero) pairs.
+template <int BITS, int BN>
+struct Stage {
+  static constexpr int kX = BN * 128;
+  static constexpr int kP = kBM * 16 * BITS;
+  static constexpr int kSZ = kBM * 4;
+  static constexpr int kBytes = ((kX + kP + kSZ) + 1023) & ~1023;
+  // stages: what fits, at most 12 (the ring covers the latency of the loads: a step takes 0.3 to
+  // 0.6 us, a load from HBM through both rings to the MMA's end about 3 us)
+  static constexpr int kFit = (232448 - 2048) / kBytes;
+  static constexpr int kS = kFit < 12 ? kFit : 12;
+};
+template <int BITS, int BN>
+constexpr int ring_smem_bytes() { return Stage<BITS, BN>::kS * Stage<BITS, BN>::kBytes + 1024 /*barriers*/ + 1024 /*align slack*/; }
+
+// How the tiles of a product become CTA pairs: `whole` tiles take one pair each; each of the others
+// is split `splits` ways over its steps (`steps` a split).  Pairs are dispatched in index order, so
+// the split tiles run last.  The plain order would leave the last wave short: T tiles on P pairs take
+// ceil(T / P) tile times, with the last T mod P of them split over the idle pairs about T / P.
 struct TileSplit {
   int tiles, whole, splits, steps;
-  int ctas() const { return whole + (tiles - whole) * splits; }
+  int pairs() const { return whole + (tiles - whole) * splits; }
 };
-struct TileOf {   // a CTA's part
+struct TileOf {   // a pair's part
   int tile, split, n_splits, first, steps;
 };
-__device__ __forceinline__ TileOf tile_of(const TileSplit& p, int cta, int all_steps) {
-  TileOf t = {cta, 0, 1, 0, all_steps};
-  if (cta >= p.whole) {
-    const int u = cta - p.whole;
+__device__ __forceinline__ TileOf tile_of(const TileSplit& p, int pair, int all_steps) {
+  TileOf t = {pair, 0, 1, 0, all_steps};
+  if (pair >= p.whole) {
+    const int u = pair - p.whole;
     t.tile = p.whole + u / p.splits;
     t.split = u % p.splits;
     t.n_splits = p.splits;
@@ -53,9 +70,9 @@ __device__ __forceinline__ TileOf tile_of(const TileSplit& p, int cta, int all_s
   }
   return t;
 }
-// fp32 partials of the split tiles: [split][tile - whole][token of the tile][MMA row]
-__device__ __forceinline__ size_t partial_at(const TileSplit& p, int split, int tile, int BN) {
-  return ((size_t)split * (p.tiles - p.whole) + (tile - p.whole)) * BN * kBM;
+// fp32 partials of the split tiles: [split][tile - whole][CTA of the pair][token of the tile][MMA row]
+__device__ __forceinline__ size_t partial_at(const TileSplit& p, int split, int tile, int rank, int BN) {
+  return (((size_t)split * (p.tiles - p.whole) + (tile - p.whole)) * 2 + rank) * BN * kBM;
 }
 
 struct GatedMaps {
@@ -71,7 +88,7 @@ struct GatedGemmParams {
   float* ws;                 // split partials
   int* status;
   int N, K, M, G, act;
-  int rts;                   // row tiles (64 output rows each); tile = token tile * rts + row tile
+  int rts;                   // row tiles (128 output rows a pair); tile = token tile * rts + row tile
   TileSplit split;
   int nw;                    // weak steps: 64 columns of each layer's weak block
   long long wait_limit;
@@ -91,31 +108,39 @@ __device__ __forceinline__ void gated_store(const GatedGemmParams& p, size_t o, 
   }
 }
 
-// The prefill kernel over interleaved rows: MMA rows 32 q .. 32 q + 15 are gate rows n0 + 16 q ..,
-// rows 32 q + 16 .. 32 q + 31 the up rows of the same outputs.  Lanes l and l + 16 of a warp then
-// hold both projections of one output, so the epilogue pairs them with a shuffle; half of the
-// columns are finished by either lane.  Weak step w: columns 64 w .. 64 w + 63 of the gate's weak
-// block against its gathered activations in the first half of the step's K, the up layer's in the
-// second half, each with zeros in the other layer's rows.
-// The 16 A-operand warps work in GR groups on different steps (GR = 2: a warp's chain of barrier,
-// unpack and tensor-memory store for one step overlaps the other group's).
-template <int BITS, int BN, int S, int GR>
-__global__ void __launch_bounds__(32 * (2 + kDW), 1)
+// The prefill kernel over interleaved rows and SM pairs.  MMA rows 32 q .. 32 q + 15 of a CTA are
+// gate rows n0 + 16 q .., rows 32 q + 16 .. 32 q + 31 the up rows of the same outputs.  Lanes l and
+// l + 16 of a warp then hold both projections of one output, so the epilogue pairs them with a
+// shuffle; half of the columns are finished by either lane.  Weak step w: columns 64 w .. 64 w + 63
+// of the gate's weak block against its gathered activations in the first half of the step's K, the
+// up layer's in the second half, each with zeros in the other layer's rows.
+// A cluster of two CTAs computes 256 MMA rows x BN tokens with cta_group::2: each CTA unpacks its
+// own 128 rows and holds half of the tokens, which halves the activations' traffic from L2 (at 256
+// tokens a lone CTA would want 64 KB a step, 17 TB/s over the GPU) and their room in the ring.
+//   warp 0      TMA producer of the CTA's ring (freed by the MMAs' commit in both CTAs)
+//   warp 1      tensor memory; in the even CTA the MMA-issuing thread
+//   warps 2-17  A operand, in kGR groups on alternate steps: wait for the stage's loads, unpack, store
+//               to one of kS2 tensor-memory stages, one arrival per warp on the even CTA's barrier
+//               (after the wait for the loads, so the barrier covers those too); then the epilogue
+template <int BITS, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (2 + kDW), 1)
 k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ GatedGemmParams p) {
-  using L = Smem<BITS, BN>;
+  using L = Stage<BITS, BN>;
+  constexpr int S = L::kS;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * L::kStage);
-  uint64_t* full = bars;            // [S] TMA landed
-  uint64_t* empty = bars + S;       // [S] MMAs of the stage done
-  uint64_t* afull = bars + 2 * S;   // [S] A tile written to tensor memory
-  uint64_t* accf = bars + 3 * S;    // accumulator complete
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 1);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * L::kBytes);
+  uint64_t* full = bars;              // [S] TMA landed
+  uint64_t* empty = bars + S;         // [S] MMAs of the stage done
+  uint64_t* afull = bars + 2 * S;     // [kS2] A stage written in both CTAs (the even CTA's is used)
+  uint64_t* accf = bars + 2 * S + kS2;   // accumulator complete
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + kS2 + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const TileOf to = tile_of(p.split, blockIdx.x, p.K / kStepCodes);
-  const int n0 = (to.tile % p.rts) * kHalfRows;   // first output row
-  const int m0 = (to.tile / p.rts) * BN;          // first token
+  const int rank = (int)cluster_ctarank();
+  const TileOf to = tile_of(p.split, blockIdx.x >> 1, p.K / kStepCodes);
+  const int n0 = ((to.tile % p.rts) * 2 + rank) * kHalfRows;   // first output row of this CTA
+  const int m0 = (to.tile / p.rts) * BN;                       // first token
   const int kb0 = to.first, nD = to.steps;        // dense steps of this split
   const int nK = nD + (to.split == to.n_splits - 1 ? p.nw : 0);   // + the weak steps (last split)
   const bool per_group = p.G > 1;
@@ -124,18 +149,19 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&afull[s], 32 * kDW / GR);
     }
+    for (int s = 0; s < kS2; ++s) mbar_init(&afull[s], 2 * kDW / kGR);   // a lane of each warp, both CTAs
     mbar_init(accf, 1);
     fence_mbar_init();
     prefetch_tmap(&maps.x);
     prefetch_tmap(&maps.p[0]);
     prefetch_tmap(&maps.p[1]);
   }
-  if (warp == 1) tmem_alloc(tmem_slot, tmem_cols<BN, S>());
+  if (warp == 1) tmem_alloc_pair(tmem_slot, kTmemCols);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
+  cluster_sync();   // both CTAs' barriers and tensor memory are ready
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -143,13 +169,14 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
     if (lane == 0) {
       // ---------------- TMA producer ----------------
       const uint32_t kDense = L::kX + L::kP + (per_group ? L::kSZ : 0);
+      const int mt = m0 + rank * (BN / 2);   // this CTA's tokens
       bool ok = true;
       int issued = 0;
       for (int i = 0; i < nK && ok; ++i) {
         const int s = i % S, u = i / S;
         if (u > 0) ok = mbar_wait(&empty[s], (u - 1) & 1, p.status, p.wait_limit);
         if (!ok) break;
-        unsigned char* st = smem + s * L::kStage;
+        unsigned char* st = smem + s * L::kBytes;
         if (i < nD) {
           const int kb = kb0 + i;
           mbar_arrive_expect_tx(&full[s], kDense);
@@ -158,14 +185,14 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
             tma_load_3d(st + L::kX + l * (L::kP / 2), &maps.p[l], &full[s], 0, kb, n0 / 16);
             if (per_group) tma_load_3d(st + L::kX + L::kP + l * (L::kSZ / 2), &maps.sz[l], &full[s], 0, kb, n0 / 16);
           }
-          tma_load_2d(st, &maps.x, &full[s], kb * kStepCodes, m0);
-          tma_load_2d(st + BN * 128, &maps.x, &full[s], kb * kStepCodes + 64, m0);
+          tma_load_2d(st, &maps.x, &full[s], kb * kStepCodes, mt);
+          tma_load_2d(st + BN * 64, &maps.x, &full[s], kb * kStepCodes + 64, mt);
         } else {
           const int c0 = (i - nD) * 64;
           if (i == nD) asm volatile("griddepcontrol.wait;" ::: "memory");   // the gathered activations
           mbar_arrive_expect_tx(&full[s], L::kX);
-          tma_load_2d(st, &maps.xw[0], &full[s], c0, m0);
-          tma_load_2d(st + BN * 128, &maps.xw[1], &full[s], c0, m0);
+          tma_load_2d(st, &maps.xw[0], &full[s], c0, mt);
+          tma_load_2d(st + BN * 64, &maps.xw[1], &full[s], c0, mt);
         }
         issued = i + 1;
       }
@@ -174,72 +201,61 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
         mbar_wait(&full[i % S], (i / S) & 1, p.status, p.wait_limit);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       // ---------------- MMA issuer ----------------
-      // (one base descriptor plus per-stage and per-slice offsets; the A stage's barrier implies
-      // the TMA's, see the prefill kernel)
-      constexpr uint32_t idesc = idesc_f16_f32(kBM, BN);
+      // (one base descriptor plus per-stage and per-slice offsets, see the prefill kernel)
+      constexpr uint32_t idesc = idesc_f16_f32(2 * kBM, BN);
       const uint64_t dbase = desc_sw128_kmajor(smem_u32(smem));
       bool ok = true;
+      int s = 0;
       for (int i = 0; i < nK && ok; ++i) {
-        const int s = i % S, u = i / S;
-        ok = mbar_wait(&afull[s], u & 1, p.status, p.wait_limit);
+        ok = mbar_wait(&afull[i % kS2], (i / kS2) & 1, p.status, p.wait_limit);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t ds = dbase + (uint64_t)((s * L::kStage) >> 4);
-        const uint32_t at = tmem + BN + 64 * s;
+        const uint64_t ds = dbase + (uint64_t)((s * L::kBytes) >> 4);
+        const uint32_t at = tmem + BN + 64 * (i % kS2);
         if (i < nD) {
-          mma_f16_ts(tmem, at, ds, idesc, i != 0);
+          mma_f16_ts_pair(tmem, at, ds, idesc, i != 0);
           #pragma unroll
           for (int kk = 1; kk < 8; ++kk)
-            mma_f16_ts(tmem, at + 8 * kk, ds + (uint64_t)((((kk >> 2) * BN * 128) + (kk & 3) * 32) >> 4), idesc, 1u);
+            mma_f16_ts_pair(tmem, at + 8 * kk, ds + (uint64_t)((((kk >> 2) * BN * 64) + (kk & 3) * 32) >> 4), idesc, 1u);
         } else {   // only the slices that hold weak columns
           #pragma unroll 1
           for (int kk = 0; kk < 8; ++kk)
             if ((i - nD) * 64 + (kk & 3) * 16 < p.k_ld[kk >> 2])
-              mma_f16_ts(tmem, at + 8 * kk, ds + (uint64_t)((((kk >> 2) * BN * 128) + (kk & 3) * 32) >> 4), idesc, 1u);
+              mma_f16_ts_pair(tmem, at + 8 * kk, ds + (uint64_t)((((kk >> 2) * BN * 64) + (kk & 3) * 32) >> 4), idesc, 1u);
         }
-        mma_commit(&empty[s]);
+        mma_commit_pair(&empty[s]);
+        if (++s == S) s = 0;
       }
-      mma_commit(accf);
+      mma_commit_pair(accf);
     }
   } else {
     // ---------------- A operand ----------------
-    // kDW / GR warps of a group, NSL = kDW / GR / 4 per lane quarter; thread (MMA row r, slab jh)
+    // kDW / kGR warps of a group, NSL = kDW / kGR / 4 per lane quarter; thread (MMA row r, slab jh)
     // writes codes 8 U jh .. 8 U jh + 8 U - 1 of its row (U = 16 / NSL), as in the prefill kernel
-    constexpr int NSL = kDW / GR / 4, U = 16 / NSL;
-    const int quarter = warp & 3, aw = warp - 2, grp = aw / (kDW / GR), jh = (aw % (kDW / GR)) >> 2;
+    constexpr int NSL = kDW / kGR / 4, U = 16 / NSL;
+    const int quarter = warp & 3, aw = warp - 2, grp = aw / (kDW / kGR), jh = (aw % (kDW / kGR)) >> 2;
     const int lay = lane >> 4, tr = 16 * quarter + (lane & 15);   // layer and row of the tile
     const int orow = n0 + tr;
     const int row = min(orow, p.N - 1);
     const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
-    uint32_t s2 = 0, scl[3], nz[3];
-    constexpr float kOff[3] = {1.f, BITS == 3 ? 8.f : 16.f, 64.f};
-    scl[0] = h2_splat(1.f);
-    scl[1] = h2_splat(1.f / kOff[1]);
-    scl[2] = h2_splat(1.f / kOff[2]);
-    auto set_sz = [&](__half sh, __half zh) {
-      const uint32_t su = __half_as_ushort(sh);
-      const float z = __half2float(zh);
-      s2 = su | (su << 16);
-      #pragma unroll
-      for (int c = 0; c < 3; ++c) nz[c] = h2_splat(-(1024.f / kOff[c] + z));
-    };
-    if (!per_group) set_sz(p.scales[lay][row], p.zeros[lay][row]);
+    RowDq<BITS> dq;
+    if (!per_group)
+      dq.set((uint32_t)__half_as_ushort(p.scales[lay][row]) | (uint32_t)__half_as_ushort(p.zeros[lay][row]) << 16);
     bool ok = true;
-    for (int i = grp; i < nK && ok; i += GR) {
+    for (int i = grp; i < nK && ok; i += kGR) {
       const int s = i % S, u = i / S;
-      ok = mbar_wait(&full[s], u & 1, p.status, p.wait_limit);   // (also: the stage's previous MMAs are done)
+      ok = mbar_wait(&full[s], u & 1, p.status, p.wait_limit);
+      if (i >= kS2) ok = mbar_wait(&empty[(i - kS2) % S], ((i - kS2) / S) & 1, p.status, p.wait_limit) && ok;   // the A stage's MMAs
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      const unsigned char* st = smem + s * L::kStage;
-      const uint32_t at = tmem + lane_base + BN + 64 * s + 4 * U * jh;
+      const unsigned char* st = smem + s * L::kBytes;
+      const uint32_t at = tmem + lane_base + BN + 64 * (i % kS2) + 4 * U * jh;
       uint32_t d[U / 4][16];
       if (i < nD) {
-        if (per_group) {
-          const __half2 sz = *reinterpret_cast<const __half2*>(st + L::kX + L::kP + lay * (L::kSZ / 2) + tr * 4);
-          set_sz(__low2half(sz), __high2half(sz));
-        }
+        if (per_group) dq.set(*reinterpret_cast<const uint32_t*>(st + L::kX + L::kP + lay * (L::kSZ / 2) + tr * 4));
         const uint4* pw = reinterpret_cast<const uint4*>(st + L::kX + lay * (L::kP / 2) + tr * 16 * BITS);
         uint32_t w[4 * BITS];
         #pragma unroll
@@ -253,7 +269,7 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
           for (int ju = 0; ju < U; ++ju)
             #pragma unroll
             for (int q = 0; q < 4; ++q)
-              d[ju >> 2][4 * (ju & 3) + q] = dequant_pair<BITS>(w + q * BITS, U * SL + ju, s2, scl, nz);
+              d[ju >> 2][4 * (ju & 3) + q] = dequant<BITS>(w + q * BITS, U * SL + ju, dq);
         };
         if constexpr (NSL == 2) {
           if (jh == 0) units(std::integral_constant<int, 0>{});
@@ -281,7 +297,8 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
       for (int h = 0; h < U / 4; ++h) tmem_st16(at + 16 * h, d[h]);
       tmem_st_wait();
       tc_fence_before();
-      if (!(p.skip_arrive && i == 0 && threadIdx.x == 64)) mbar_arrive(&afull[s]);
+      __syncwarp();
+      if (lane == 0 && !(p.skip_arrive && i == 0 && threadIdx.x == 64)) mbar_arrive_remote(&afull[i % kS2], 0);
     }
 
     // ---------------- epilogue ----------------
@@ -296,7 +313,7 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
       tmem_ld_wait();
       if (!acc_ok) continue;
       if (to.n_splits > 1) {   // this split's fp32 partials
-        float* w = p.ws + partial_at(p.split, to.split, to.tile, BN) + (size_t)c0 * kBM + 32 * quarter + lane;
+        float* w = p.ws + partial_at(p.split, to.split, to.tile, rank, BN) + (size_t)c0 * kBM + 32 * quarter + lane;
         #pragma unroll
         for (int j = 0; j < 16; ++j) w[j * kBM] = __uint_as_float(v[j]);
       } else {
@@ -314,10 +331,10 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
 
   tc_fence_before();
   __syncthreads();
+  cluster_sync();   // neither CTA leaves, or frees tensor memory, while the pair's MMAs may use it
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, tmem_cols<BN, S>());
-    tmem_relinquish();
+    tmem_free_pair(tmem, kTmemCols);
   }
 }
 
@@ -343,12 +360,13 @@ __global__ void k_gated_gather(const __half* __restrict__ x, int M, int K, const
 __global__ void k_gated_reduce(const __grid_constant__ GatedGemmParams p, int BN) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n_tiles = p.split.tiles - p.split.whole;
-  const size_t n = (size_t)n_tiles * BN * kHalfRows, stride = (size_t)n_tiles * BN * kBM;
+  const size_t n = (size_t)n_tiles * 2 * BN * kHalfRows, stride = (size_t)n_tiles * 2 * BN * kBM;
   for (size_t e = (size_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (size_t)gridDim.x * blockDim.x) {
-    const int r = (int)(e % kHalfRows), tile = p.split.whole + (int)(e / kHalfRows / BN), t0 = (int)(e / kHalfRows % BN);
-    const int row = (tile % p.rts) * kHalfRows + r, t = (tile / p.rts) * BN + t0;
+    const int r = (int)(e % kHalfRows), t0 = (int)(e / kHalfRows % BN), u = (int)(e / kHalfRows / BN);
+    const int tile = p.split.whole + u / 2, rank = u % 2;
+    const int row = ((tile % p.rts) * 2 + rank) * kHalfRows + r, t = (tile / p.rts) * BN + t0;
     if (row >= p.N || t >= p.M) continue;
-    const float* w = p.ws + partial_at(p.split, 0, tile, BN) + (size_t)t0 * kBM + 32 * (r / 16) + r % 16;
+    const float* w = p.ws + partial_at(p.split, 0, tile, rank, BN) + (size_t)t0 * kBM + 32 * (r / 16) + r % 16;
     float gs = w[0], us = w[16];
     for (int z = 1; z < p.split.splits; ++z) {
       gs += w[z * stride];
@@ -372,9 +390,6 @@ __global__ void k_gated_reduce(const __grid_constant__ GatedGemmParams p, int BN
 // The weak columns' codes give exactly 0; their products with the fp16 weak blocks come from
 // k_gated_igw, running beside this kernel, and are added in fp32 in the epilogue of a tile's first
 // split, so that a column that is weak in one layer and packed in the other is rounded once.
-template <int BITS, int BN, int S>
-constexpr int ig2_smem_bytes() { return S * Smem<BITS, BN>::kStage + 1024 + 1024; }
-
 struct GatedIgMaps {
   CUtensorMap dy[2], p[2], sz[2], dx;
 };
@@ -382,7 +397,7 @@ struct GatedIgParams {
   float* ws;        // split partials
   int* status;
   int N, K, M, group;
-  TileSplit split;  // tile = token tile * (K / 128) + column block; steps: 128 rows, the gate's first
+  TileSplit split;  // tile = token tile * ceil(K / 256) + pair of column blocks; steps: 128 rows, the gate's first
   long long wait_limit;
   const float* wk[2];   // the weak columns' products, [row split][slot][M]
   const int32_t* idx[2];
@@ -424,7 +439,6 @@ __device__ __forceinline__ void ig_load_words(uint32_t a, uint32_t (&w)[BITS]) {
 // (packed rows) and `sz` ((scale, zero) pairs), to tensor memory at `at` (lane quarter Q).
 template <int BITS, int Q, int RG>
 __device__ __forceinline__ void ig_form(uint32_t pk, uint32_t sz, uint32_t at) {
-  constexpr int NC = BITS == 3 ? 3 : 2;
   #pragma unroll
   for (int b = 0; b < RG / 4; ++b) {
     uint32_t v[2][8];   // [16-column half][16x128b registers of four row groups]
@@ -433,42 +447,38 @@ __device__ __forceinline__ void ig_form(uint32_t pk, uint32_t sz, uint32_t at) {
       const int rg = 4 * b + i;
       uint32_t w[BITS];
       ig_load_words<BITS, Q>(pk + rg * 8 * 16 * BITS, w);
-      const uint32_t z = lds_u1(sz + rg * 32);
-      const uint32_t s2 = __byte_perm(z, z, 0x1010), z2 = __byte_perm(z, z, 0x3232);
-      uint32_t scl[NC], nz[NC];
-      #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        scl[c] = ((uint32_t)(15 - class_off<BITS>(c)) << 10) * 0x00010001u;                                // 2^-o
-        nz[c] = h2_sub((0x8000u | ((uint32_t)(25 - class_off<BITS>(c)) << 10)) * 0x00010001u, z2);   // -(2^(10 - o) + z)
-      }
+      RowDq<BITS> dq;
+      dq.set(lds_u1(sz + rg * 32));
       #pragma unroll
       for (int p = 0; p < 4; ++p)
-        v[p >> 1][2 * i + (p & 1)] = movmatrix(dequant_pair<BITS>(w, 4 * Q + p, s2, scl, nz));
+        v[p >> 1][2 * i + (p & 1)] = movmatrix(dequant<BITS>(w, 4 * Q + p, dq));
     }
     #pragma unroll
     for (int h = 0; h < 2; ++h) tmem_st_16x128b_x4(at + ((uint32_t)(16 * h) << 16) + 16 * b, v[h]);
   }
 }
 
-template <int BITS, int BN, int S, int GR>
-__global__ void __launch_bounds__(32 * (2 + kDW), 1)
+template <int BITS, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (2 + kDW), 1)
 k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ GatedIgParams p) {
-  using L = Smem<BITS, BN>;
+  using L = Stage<BITS, BN>;
+  constexpr int S = L::kS;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * L::kStage);
-  uint64_t* full = bars;            // [S] TMA landed
-  uint64_t* empty = bars + S;       // [S] MMAs of the stage done
-  uint64_t* afull = bars + 2 * S;   // [S] A tile written to tensor memory
-  uint64_t* accf = bars + 3 * S;    // accumulator complete
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * S + 1);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * L::kBytes);
+  uint64_t* full = bars;              // [S] TMA landed
+  uint64_t* empty = bars + S;         // [S] MMAs of the stage done
+  uint64_t* afull = bars + 2 * S;     // [kS2] A stage written in both CTAs (the even CTA's is used)
+  uint64_t* accf = bars + 2 * S + kS2;   // accumulator complete
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + kS2 + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int Kb = p.K / kStepCodes;
+  const int rank = (int)cluster_ctarank();
+  const int Kb = p.K / kStepCodes, Kp = (Kb + 1) / 2;   // column blocks, and pairs of them
   const int nR = (p.N + 127) / 128;     // row steps of one layer
-  const TileOf to = tile_of(p.split, blockIdx.x, 2 * nR);
-  const int b = to.tile % Kb;           // column block (128 columns)
-  const int m0 = (to.tile / Kb) * BN;   // first token
+  const TileOf to = tile_of(p.split, blockIdx.x >> 1, 2 * nR);
+  const int b = (to.tile % Kp) * 2 + rank;   // this CTA's column block (Kb odd: the last has none; it loads zeros, stores nothing)
+  const int m0 = (to.tile / Kp) * BN;        // first token
   const int nK = to.steps;
   const int grp = (b * kStepCodes) / p.group;
 
@@ -476,8 +486,8 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&afull[s], 32 * kDW / GR);
     }
+    for (int s = 0; s < kS2; ++s) mbar_init(&afull[s], 2 * kDW / kGR);   // a lane of each warp, both CTAs
     mbar_init(accf, 1);
     fence_mbar_init();
     #pragma unroll
@@ -487,73 +497,79 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
       prefetch_tmap(&maps.sz[l]);
     }
   }
-  if (warp == 1) tmem_alloc(tmem_slot, tmem_cols<BN, S>());
+  if (warp == 1) tmem_alloc_pair(tmem_slot, kTmemCols);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
+  cluster_sync();   // both CTAs' barriers and tensor memory are ready
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
     if (lane == 0) {
       // ---------------- TMA producer ----------------
+      const int mt = m0 + rank * (BN / 2);   // this CTA's tokens
       bool ok = true;
       int issued = 0;
       for (int i = 0; i < nK && ok; ++i) {
         const int s = i % S, u = i / S;
         if (u > 0) ok = mbar_wait(&empty[s], (u - 1) & 1, p.status, p.wait_limit);
         if (!ok) break;
-        unsigned char* st = smem + s * L::kStage;
+        unsigned char* st = smem + s * L::kBytes;
         const int l = to.first + i >= nR, rb = to.first + i - (l ? nR : 0);
         mbar_arrive_expect_tx(&full[s], L::kX + L::kP + L::kSZ);
         tma_load_3d(st + L::kX, &maps.p[l], &full[s], 0, b, rb * 8);
         tma_load_3d(st + L::kX + L::kP, &maps.sz[l], &full[s], 0, grp, rb * 8);
-        tma_load_2d(st, &maps.dy[l], &full[s], rb * 128, m0);
-        tma_load_2d(st + BN * 128, &maps.dy[l], &full[s], rb * 128 + 64, m0);
+        tma_load_2d(st, &maps.dy[l], &full[s], rb * 128, mt);
+        tma_load_2d(st + BN * 64, &maps.dy[l], &full[s], rb * 128 + 64, mt);
         issued = i + 1;
       }
       for (int i = (issued > S ? issued - S : 0); i < issued; ++i)
         mbar_wait(&full[i % S], (i / S) & 1, p.status, p.wait_limit);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       // ---------------- MMA issuer ----------------
-      constexpr uint32_t idesc = idesc_f16_f32(kBM, BN);
+      // (one base descriptor plus per-stage and per-slice offsets, see the prefill kernel)
+      constexpr uint32_t idesc = idesc_f16_f32(2 * kBM, BN);
       const uint64_t dbase = desc_sw128_kmajor(smem_u32(smem));
       bool ok = true;
+      int s = 0;
       for (int i = 0; i < nK && ok; ++i) {
-        const int s = i % S, u = i / S;
-        ok = mbar_wait(&afull[s], u & 1, p.status, p.wait_limit);
+        ok = mbar_wait(&afull[i % kS2], (i / kS2) & 1, p.status, p.wait_limit);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t ds = dbase + (uint64_t)((s * L::kStage) >> 4);
-        const uint32_t at = tmem + BN + 64 * s;
-        mma_f16_ts(tmem, at, ds, idesc, i != 0);
+        const uint64_t ds = dbase + (uint64_t)((s * L::kBytes) >> 4);
+        const uint32_t at = tmem + BN + 64 * (i % kS2);
+        mma_f16_ts_pair(tmem, at, ds, idesc, i != 0);
         #pragma unroll
         for (int kk = 1; kk < 8; ++kk)
-          mma_f16_ts(tmem, at + 8 * kk, ds + (uint64_t)((((kk >> 2) * BN * 128) + (kk & 3) * 32) >> 4), idesc, 1u);
-        mma_commit(&empty[s]);
+          mma_f16_ts_pair(tmem, at + 8 * kk, ds + (uint64_t)((((kk >> 2) * BN * 64) + (kk & 3) * 32) >> 4), idesc, 1u);
+        mma_commit_pair(&empty[s]);
+        if (++s == S) s = 0;
       }
-      mma_commit(accf);
+      mma_commit_pair(accf);
     }
   } else {
     // ---------------- A operand: W_hat^T ----------------
     // group grp of the steps; within it lane quarter = warp % 4 (32 columns) and row slab jh
-    constexpr int NSL = kDW / GR / 4, RG = 16 / NSL;   // 8-row groups of a warp's slab
-    const int quarter = warp & 3, aw = warp - 2, gr = aw / (kDW / GR), jh = (aw % (kDW / GR)) >> 2;
+    constexpr int NSL = kDW / kGR / 4, RG = 16 / NSL;   // 8-row groups of a warp's slab
+    const int quarter = warp & 3, aw = warp - 2, gr = aw / (kDW / kGR), jh = (aw % (kDW / kGR)) >> 2;
     const int g = lane >> 2, t = lane & 3;
     const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
     const uint32_t sm = smem_u32(smem);
     bool ok = true;
-    for (int i = gr; i < nK && ok; i += GR) {
+    for (int i = gr; i < nK && ok; i += kGR) {
       const int s = i % S, u = i / S;
-      ok = __all_sync(0xffffffffu, mbar_wait(&full[s], u & 1, p.status, p.wait_limit));   // (also: the stage's previous MMAs are done)
+      ok = mbar_wait(&full[s], u & 1, p.status, p.wait_limit);
+      if (i >= kS2) ok = mbar_wait(&empty[(i - kS2) % S], ((i - kS2) / S) & 1, p.status, p.wait_limit) && ok;   // the A stage's MMAs
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t st = sm + s * L::kStage;
+      const uint32_t st = sm + s * L::kBytes;
       const uint32_t pk = st + L::kX + (8 * RG * jh + g) * 16 * BITS + t * 4 * BITS;
       const uint32_t sz = st + L::kX + L::kP + (8 * RG * jh + g) * 4;
-      const uint32_t at = tmem + lane_base + BN + 64 * s + 4 * RG * jh;
+      const uint32_t at = tmem + lane_base + BN + 64 * (i % kS2) + 4 * RG * jh;
       switch (quarter) {
         case 0: ig_form<BITS, 0, RG>(pk, sz, at); break;
         case 1: ig_form<BITS, 1, RG>(pk, sz, at); break;
@@ -562,7 +578,8 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&afull[s]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(&afull[i % kS2], 0);
     }
 
     // ---------------- epilogue ----------------
@@ -574,10 +591,10 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
     __half* s_out = reinterpret_cast<__half*>(smem);
     // the weak columns of this block in either layer: their products' row splits added in order
     // into shared memory (behind the output tile; those that do not fit are added from global)
-    constexpr int kWkCap = (S * L::kStage - BN * kStepCodes * 2) / (BN * 4);
+    constexpr int kWkCap = (S * L::kBytes - BN * kStepCodes * 2) / (BN * 4);
     int slot[2] = {-1, -1}, at_wk[2] = {0, 0}, n_weak = 0;   // this column's weak slot, and its place
     float* s_wk = reinterpret_cast<float*>(smem + BN * kStepCodes * 2);   // [weak column][BN]
-    if (to.split == 0) {
+    if (to.split == 0 && b < Kb) {
       #pragma unroll
       for (int l = 0; l < 2; ++l) {
         const int first = p.k[l] > 0 ? (int)(p.blk[l][b] >> 16) : 0, cnt = p.k[l] > 0 ? (int)(p.blk[l][b] & 0xFFFFu) : 0;
@@ -624,7 +641,7 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
         }
       if (to.n_splits > 1) {
         if (acc_ok) {
-          float* w = p.ws + partial_at(p.split, to.split, to.tile, BN) + (size_t)c0 * kBM + j;
+          float* w = p.ws + partial_at(p.split, to.split, to.tile, rank, BN) + (size_t)c0 * kBM + j;
           #pragma unroll
           for (int tk = 0; tk < 16; ++tk) w[tk * kBM] = __uint_as_float(v[tk]);
         }
@@ -637,7 +654,7 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
     if (to.n_splits == 1) {
       fence_proxy_async_smem();          // the tile, written by the generic proxy, to the TMA
       named_bar_sync(1, 32 * kDW);       // every A thread's part of the tile is written
-      if (warp == 2 && lane == 0 && acc_ok) {
+      if (warp == 2 && lane == 0 && acc_ok && b < Kb) {
         tma_store_2d(&maps.dx, s_out, b * kStepCodes, m0);
         bulk_commit();
         bulk_wait_read0();               // shared memory read out before the CTA may exit
@@ -647,28 +664,28 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
 
   tc_fence_before();
   __syncthreads();
+  cluster_sync();   // neither CTA leaves, or frees tensor memory, while the pair's MMAs may use it
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, tmem_cols<BN, S>());
-    tmem_relinquish();
+    tmem_free_pair(tmem, kTmemCols);
   }
 }
 
 // dx of the split tiles = fp16_rn(their partials added in split order)
 __global__ void k_gated_ig_reduce(const __grid_constant__ GatedIgParams p, int BN, __half* __restrict__ dx) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n_tiles = p.split.tiles - p.split.whole, Kb = p.K / kStepCodes;
-  const size_t n = (size_t)n_tiles * BN * kBM;
+  const int n_tiles = p.split.tiles - p.split.whole, Kb = p.K / kStepCodes, Kp = (Kb + 1) / 2;
+  const size_t n = (size_t)n_tiles * 2 * BN * kBM;
   for (size_t e = 4 * ((size_t)blockIdx.x * blockDim.x + threadIdx.x); e < n; e += 4 * (size_t)gridDim.x * blockDim.x) {
-    const int c = (int)(e % kBM), t0 = (int)(e / kBM % BN), tile = p.split.whole + (int)(e / kBM / BN);
-    const int t = (tile / Kb) * BN + t0;
-    if (t >= p.M) continue;
+    const int c = (int)(e % kBM), t0 = (int)(e / kBM % BN), u = (int)(e / kBM / BN), tile = p.split.whole + u / 2;
+    const int b = (tile % Kp) * 2 + u % 2, t = (tile / Kp) * BN + t0;
+    if (t >= p.M || b >= Kb) continue;
     float4 v = *reinterpret_cast<const float4*>(p.ws + e);
     for (int z = 1; z < p.split.splits; ++z) {
       const float4 w = *reinterpret_cast<const float4*>(p.ws + (size_t)z * n + e);
       v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
     }
-    __half2* o = reinterpret_cast<__half2*>(dx + (size_t)t * p.K + (tile % Kb) * kStepCodes + c);
+    __half2* o = reinterpret_cast<__half2*>(dx + (size_t)t * p.K + b * kStepCodes + c);
     o[0] = __floats2half2_rn(v.x, v.y);
     o[1] = __floats2half2_rn(v.z, v.w);
   }
@@ -782,10 +799,11 @@ unsigned blocks_for(size_t n, int threads, unsigned most) {
 // the MMAs above, so one wide tile beats two narrower ones.
 int gated_tile_tokens(int M) { return M <= 64 ? 64 : M <= 128 ? 128 : 256; }
 
-// The split of T tiles of `steps` steps over P SMs (see TileSplit): at least 4 steps a split, and
+// The split of T tiles of `steps` steps over the SM pairs (see TileSplit): at least 4 steps a split, and
 // only where the saved time, in units of a step (about 0.3 us for 64 tokens to 0.65 us for 256),
 // exceeds the partials' way through L2 and the reduction's launch (about 4 us).
-TileSplit plan_split(long long T, int steps, int BN, int P) {
+TileSplit plan_split(long long T, int steps, int BN, int sms) {
+  const int P = std::max(1, sms / 2);
   TileSplit s = {(int)T, (int)T, 1, steps};
   const int rem = (int)(T % P);
   if (rem == 0) return s;
@@ -794,7 +812,7 @@ TileSplit plan_split(long long T, int steps, int BN, int P) {
   const int per = (steps + n - 1) / n;
   n = (steps + per - 1) / per;
   const double step_us = BN == 64 ? 0.3 : BN == 128 ? 0.4 : 0.65;
-  const double cost_us = 4.0 + 2.0 * n * rem * BN * kBM * sizeof(float) / 5e6;
+  const double cost_us = 4.0 + 4.0 * n * rem * BN * kBM * sizeof(float) / 5e6;
   if ((steps - per) * step_us <= cost_us) return s;
   s.whole = (int)(T - rem);
   s.splits = n;
@@ -802,7 +820,7 @@ TileSplit plan_split(long long T, int steps, int BN, int P) {
   return s;
 }
 size_t partial_bytes(const TileSplit& s, int BN) {
-  return s.splits > 1 ? up256((size_t)s.splits * (s.tiles - s.whole) * BN * kBM * sizeof(float)) : 0;
+  return s.splits > 1 ? up256((size_t)s.splits * (s.tiles - s.whole) * 2 * BN * kBM * sizeof(float)) : 0;
 }
 
 cudaError_t launch_pdl(void* kern, dim3 grid, int threads, size_t smem, bool pdl, cudaStream_t s, void** args) {
@@ -828,7 +846,7 @@ struct FwdPlan {
 FwdPlan fwd_plan(const Layer& gate, const Layer& up, int M) {
   FwdPlan f;
   f.BN = gated_tile_tokens(M);
-  f.rts = (gate.N + kHalfRows - 1) / kHalfRows;
+  f.rts = (gate.N + 2 * kHalfRows - 1) / (2 * kHalfRows);
   f.split = plan_split((long long)f.rts * ((M + f.BN - 1) / f.BN), gate.K / kStepCodes, f.BN, layer_sm_count(gate.device));
   size_t at = 0;
   const Layer* L[2] = {&gate, &up};
@@ -841,14 +859,14 @@ FwdPlan fwd_plan(const Layer& gate, const Layer& up, int M) {
   return f;
 }
 
-template <int BITS, int BN, int S, int GR>
+template <int BITS, int BN>
 owq_status_t run_gemm(const Layer& gate, const Layer& up, int act, const __half* x, const __half* dh, __half* out0, __half* out1,
                       int M, const FwdPlan& f, unsigned char* ws, long long wait_limit, bool skip_arrive, cudaStream_t s) {
   const Layer* L[2] = {&gate, &up};
   GatedMaps maps;
   GatedGemmParams prm;
   GatherArgs ga;
-  if (!encode_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)gate.K, (uint64_t)M, (uint64_t)gate.K * 2, 64, BN,
+  if (!encode_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)gate.K, (uint64_t)M, (uint64_t)gate.K * 2, 64, BN / 2,
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return OWQ_ERR_CUDA;
   for (int l = 0; l < 2; ++l) {
@@ -860,11 +878,12 @@ owq_status_t run_gemm(const Layer& gate, const Layer& up, int act, const __half*
     ga.xw[l] = reinterpret_cast<__half*>(ws + f.xw[l]);
     ga.k[l] = L[l]->k;
     ga.k_ld[l] = prm.k_ld[l];
-    maps.xw[l] = maps.x;   // (a layer without weak columns: loaded, never multiplied)
     if (!encode_packed_3d(&maps.p[l], L[l]->packed, L[l]->K, L[l]->N, BITS, kHalfRows / 16) ||
         !encode_sz_3d(&maps.sz[l], L[l]->sz_t, L[l]->G, L[l]->N, kHalfRows / 16) ||
-        (L[l]->k > 0 && !encode_2d(&maps.xw[l], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ga.xw[l], (uint64_t)L[l]->k_ld, (uint64_t)M,
-                                   (uint64_t)L[l]->k_ld * 2, 64, BN, CU_TENSOR_MAP_SWIZZLE_128B)))
+        // (a layer without weak columns: x itself, loaded and never multiplied)
+        !encode_2d(&maps.xw[l], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, L[l]->k > 0 ? ga.xw[l] : x,
+                   (uint64_t)(L[l]->k > 0 ? L[l]->k_ld : gate.K), (uint64_t)M, (uint64_t)(L[l]->k > 0 ? L[l]->k_ld : gate.K) * 2, 64,
+                   BN / 2, CU_TENSOR_MAP_SWIZZLE_128B))
       return OWQ_ERR_CUDA;
   }
   prm.dh = dh;
@@ -878,11 +897,11 @@ owq_status_t run_gemm(const Layer& gate, const Layer& up, int act, const __half*
   prm.rts = f.rts;
   prm.split = f.split;
   prm.ws = reinterpret_cast<float*>(ws + f.ws);
-  auto kern = k_gated_gemm<BITS, BN, S, GR>;
-  constexpr int smem = smem_bytes<BITS, BN, S>();
-  static_assert(smem <= 232448, "shared memory budget");
-  static_assert(BN + 64 * S <= (int)tmem_cols<BN, S>(), "tensor memory: accumulator + A stages");
-  static_assert((232448 / smem) * tmem_cols<BN, S>() <= 512, "tensor memory per SM");
+  auto kern = k_gated_gemm<BITS, BN>;
+  constexpr int smem = ring_smem_bytes<BITS, BN>();
+  static_assert(smem <= 232448 && 2 * smem > 232448, "one CTA per SM: the tensor memory of one");
+  static_assert(BN + 64 * kS2 <= (int)kTmemCols, "tensor memory: accumulator + A stages");
+  static_assert(Stage<BITS, BN>::kS >= kS2, "an A stage's MMAs are waited for on the ring's barriers");
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
     cudaGetLastError();
     return OWQ_ERR_CUDA;
@@ -894,14 +913,14 @@ owq_status_t run_gemm(const Layer& gate, const Layer& up, int act, const __half*
   }
   // beside the gather: only the weak steps wait for it
   void* args[] = {&maps, &prm};
-  if (launch_pdl((void*)kern, dim3(f.split.ctas()), 32 * (2 + kDW), smem, ld > 0, s, args) != cudaSuccess) {
+  if (launch_pdl((void*)kern, dim3(2 * f.split.pairs()), 32 * (2 + kDW), smem, ld > 0, s, args) != cudaSuccess) {
     cudaGetLastError();
     return OWQ_ERR_CUDA;
   }
   if (f.split.splits > 1) {
     int bn = BN;
     void* rargs[] = {&prm, &bn};
-    const size_t n = (size_t)(f.split.tiles - f.split.whole) * BN * kHalfRows;
+    const size_t n = (size_t)(f.split.tiles - f.split.whole) * 2 * BN * kHalfRows;
     if (launch_pdl((void*)k_gated_reduce, dim3(blocks_for(n, 256, 4096)), 256, 0, true, s, rargs) != cudaSuccess) {
       cudaGetLastError();
       return OWQ_ERR_CUDA;
@@ -914,9 +933,9 @@ template <int BITS>
 owq_status_t dispatch_gemm(const Layer& gate, const Layer& up, int act, const __half* x, const __half* dh, __half* out0,
                            __half* out1, int M, const FwdPlan& f, unsigned char* ws, long long wl, bool skip, cudaStream_t s) {
   switch (f.BN) {
-    case 64: return run_gemm<BITS, 64, 6, 2>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
-    case 128: return run_gemm<BITS, 128, 4, 2>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
-    default: return run_gemm<BITS, 256, 3, OWQ_GR256>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
+    case 64: return run_gemm<BITS, 64>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
+    case 128: return run_gemm<BITS, 128>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
+    default: return run_gemm<BITS, 256>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
   }
 }
 
@@ -931,7 +950,7 @@ IgPlan ig_plan(const Layer& gate, const Layer& up, int M) {
   IgPlan f;
   const int sms = layer_sm_count(gate.device);
   f.BN = gated_tile_tokens(M);
-  f.split = plan_split((long long)(gate.K / kStepCodes) * ((M + f.BN - 1) / f.BN), 2 * ((gate.N + 127) / 128), f.BN, sms);
+  f.split = plan_split((long long)((gate.K / kStepCodes + 1) / 2) * ((M + f.BN - 1) / f.BN), 2 * ((gate.N + 127) / 128), f.BN, sms);
   f.ldy = (gate.N + 7) & ~7;
   size_t at = 0;
   for (int l = 0; l < 2; ++l) {
@@ -956,7 +975,7 @@ IgPlan ig_plan(const Layer& gate, const Layer& up, int M) {
   return f;
 }
 
-template <int BITS, int BN, int S, int GR>
+template <int BITS, int BN>
 owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const __half* du, __half* dx, int M, const IgPlan& f,
                     unsigned char* ws, long long wait_limit, cudaStream_t s) {
   const Layer* L[2] = {&gate, &up};
@@ -973,7 +992,7 @@ owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const 
   GatedIgwArgs wa;
   const int Kb = gate.K / kStepCodes;
   for (int l = 0; l < 2; ++l) {
-    if (!encode_2d(&maps.dy[l], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dy[l], (uint64_t)gate.N, (uint64_t)M, (uint64_t)f.ldy * 2, 64, BN,
+    if (!encode_2d(&maps.dy[l], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dy[l], (uint64_t)gate.N, (uint64_t)M, (uint64_t)f.ldy * 2, 64, BN / 2,
                    CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_packed_3d(&maps.p[l], L[l]->packed, L[l]->K, L[l]->N, BITS) ||
         !encode_sz_3d(&maps.sz[l], L[l]->sz_t, L[l]->G, L[l]->N))
@@ -999,11 +1018,9 @@ owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const 
   wa.ctiles0 = (gate.k + f.ct - 1) / f.ct;
   wa.N = gate.N; wa.ldy = f.ldy; wa.M = M; wa.per = f.wper;
   const int C = wa.ctiles0 + (up.k + f.ct - 1) / f.ct;
-  auto kern = k_gated_igemm<BITS, BN, S, GR>;
-  constexpr int smem = ig2_smem_bytes<BITS, BN, S>();
-  static_assert(smem <= 232448, "shared memory budget");
-  static_assert((232448 / smem) * tmem_cols<BN, S>() <= 512, "tensor memory per SM");
-  static_assert(BN * kStepCodes * 2 <= Smem<BITS, BN>::kStage, "output tile in the first stage");
+  auto kern = k_gated_igemm<BITS, BN>;
+  constexpr int smem = ring_smem_bytes<BITS, BN>();
+  static_assert(BN * kStepCodes * 2 <= Stage<BITS, BN>::kS * Stage<BITS, BN>::kBytes, "output tile in the stages");
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
     cudaGetLastError();
     return OWQ_ERR_CUDA;
@@ -1016,14 +1033,14 @@ owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const 
   }
   // beside the weak products: only the epilogues of blocks with weak columns wait for them
   void* args[] = {&maps, &prm};
-  if (launch_pdl((void*)kern, dim3(f.split.ctas()), 32 * (2 + kDW), smem, C > 0, s, args) != cudaSuccess) {
+  if (launch_pdl((void*)kern, dim3(2 * f.split.pairs()), 32 * (2 + kDW), smem, C > 0, s, args) != cudaSuccess) {
     cudaGetLastError();
     return OWQ_ERR_CUDA;
   }
   if (f.split.splits > 1) {
     int bn = BN;
     void* rargs[] = {&prm, &bn, &dx};
-    const size_t n = (size_t)(f.split.tiles - f.split.whole) * BN * kBM;
+    const size_t n = (size_t)(f.split.tiles - f.split.whole) * 2 * BN * kBM;
     if (launch_pdl((void*)k_gated_ig_reduce, dim3(blocks_for(n / 4, 256, 4096)), 256, 0, true, s, rargs) != cudaSuccess) {
       cudaGetLastError();
       return OWQ_ERR_CUDA;
@@ -1036,9 +1053,9 @@ template <int BITS>
 owq_status_t dispatch_ig(const Layer& gate, const Layer& up, const __half* dg, const __half* du, __half* dx, int M, const IgPlan& f,
                          unsigned char* ws, long long wl, cudaStream_t s) {
   switch (f.BN) {
-    case 64: return run_ig<BITS, 64, 6, 2>(gate, up, dg, du, dx, M, f, ws, wl, s);
-    case 128: return run_ig<BITS, 128, 4, 2>(gate, up, dg, du, dx, M, f, ws, wl, s);
-    default: return run_ig<BITS, 256, 3, OWQ_GR256>(gate, up, dg, du, dx, M, f, ws, wl, s);
+    case 64: return run_ig<BITS, 64>(gate, up, dg, du, dx, M, f, ws, wl, s);
+    case 128: return run_ig<BITS, 128>(gate, up, dg, du, dx, M, f, ws, wl, s);
+    default: return run_ig<BITS, 256>(gate, up, dg, du, dx, M, f, ws, wl, s);
   }
 }
 

@@ -25,7 +25,7 @@
 // held by several warps meet in shared memory after one barrier and are added in unit order, so
 // repeated calls give identical bits.
 #include "owq_act.cuh"
-#include "owq_format.cuh"
+#include "owq_dequant.cuh"
 #include "owq_internal.cuh"
 #include "owq_mma.cuh"
 #include "owq_sm100.cuh"
@@ -60,7 +60,6 @@ struct Unit {
   static constexpr int kBlk = 16 * BITS;              // bytes of one block of one row
   static constexpr int kTileBlk = 16 * kBlk;          // of a 16-row tile, one layer
   static constexpr int kSlices = kTileBlk / 512;      // weak slices per unit and layer
-  static constexpr int kNC = BITS == 3 ? 3 : 2;       // code offset classes
 };
 template <int BITS>
 constexpr int stage_bytes(int sub, bool pg) { return sub * 2 * (Unit<BITS>::kTileBlk + (pg ? 64 : 0)); }
@@ -88,43 +87,6 @@ __device__ __forceinline__ uint32_t lds_u1(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// A row's dequantisation constants: the scale splat and, per offset class c, -(1024 2^-o_c + z).
-// A code pair lifted as (bits | 0x6400) is 1024 + q 2^o per half; times 2^-o plus that constant
-// is q - z exactly (one fma), times s rounds once: fp16_rn(s (q - z)).
-template <int BITS>
-struct RowDq {
-  uint32_t s2, nz[Unit<BITS>::kNC];
-  __device__ __forceinline__ void set(uint32_t sz) {   // scale in the low half, zero in the high
-    s2 = __byte_perm(sz, sz, 0x1010);
-    const uint32_t z2 = __byte_perm(sz, sz, 0x3232);
-    #pragma unroll
-    for (int c = 0; c < Unit<BITS>::kNC; ++c)   // -2^(10 - o) as fp16, both halves
-      nz[c] = h2_sub((0x8000u | ((uint32_t)(25 - class_off<BITS>(c)) << 10)) * 0x00010001u, z2);
-  }
-};
-template <int BITS>
-__device__ __forceinline__ uint32_t dequant(const uint32_t (&w)[BITS], int j, const RowDq<BITS>& dq) {
-  const int c = pair_class<BITS>(j);
-  const uint32_t scl = ((uint32_t)(15 - class_off<BITS>(c)) << 10) * 0x00010001u;   // 2^-o
-  return h2_mul(h2_fma(pair_bits<BITS>(w, j) | 0x64006400u, scl, dq.nz[c]), dq.s2);
-}
-
 template <int BITS, int NT, bool PG, bool XSMEM>
 __global__ void __launch_bounds__(kWarps * 32, 1)
 k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
