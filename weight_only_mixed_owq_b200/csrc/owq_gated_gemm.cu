@@ -28,8 +28,9 @@ using namespace sm100;
 constexpr int kHalfRows = kBM / 2;     // output rows of a tile: 64 of each layer
 constexpr int kDW = 16;                // A-operand warps
 constexpr int kGR = 2;                 // groups of them, on alternate steps
-constexpr int kS2 = 4;                 // A stages in tensor memory
-constexpr uint32_t kTmemCols = 512;    // accumulator (up to 256 columns) and kS2 x 64
+constexpr uint32_t kTmemCols = 512;    // the accumulator (BN columns), then the A stages of 64 columns
+template <int BN>
+constexpr int a_stages() { return BN == 256 ? 4 : 6; }
 
 // One ring stage of a CTA: half of the step's tokens (two 128B-swizzled boxes of 64 columns), the
 // packed block of its 128 rows and their (scale, zero) pairs.
@@ -95,14 +96,14 @@ struct GatedGemmParams {
   int skip_arrive;
 };
 
-// outputs of one element; gs, us: both projections
-__device__ __forceinline__ void gated_store(const GatedGemmParams& p, size_t o, float gs, float us) {
+// outputs of one element; gs, us: both projections; dhv: its gradient (backward)
+__device__ __forceinline__ void gated_store(const GatedGemmParams& p, size_t o, float gs, float us, __half dhv) {
   if (p.dh == nullptr) {
     p.out[0][o] = __float2half_rn(act_value(p.act, gs) * us);
   } else {
     float a, da;
     act_both(p.act, gs, a, da);
-    const float dh = __half2float(p.dh[o]);
+    const float dh = __half2float(dhv);
     p.out[0][o] = __float2half_rn(dh * us * da);
     p.out[1][o] = __float2half_rn(dh * a);
   }
@@ -126,7 +127,7 @@ template <int BITS, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (2 + kDW), 1)
 k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ GatedGemmParams p) {
   using L = Stage<BITS, BN>;
-  constexpr int S = L::kS;
+  constexpr int S = L::kS, kS2 = a_stages<BN>();
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * L::kBytes);
@@ -136,7 +137,7 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
   uint64_t* accf = bars + 2 * S + kS2;   // accumulator complete
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + kS2 + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (warp: uniform)
   const int rank = (int)cluster_ctarank();
   const TileOf to = tile_of(p.split, blockIdx.x >> 1, p.K / kStepCodes);
   const int n0 = ((to.tile % p.rts) * 2 + rank) * kHalfRows;   // first output row of this CTA
@@ -201,7 +202,7 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
         mbar_wait(&full[i % S], (i / S) & 1, p.status, p.wait_limit);
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {   // the whole warp runs the loop, so that its values stay in uniform registers
       // ---------------- MMA issuer ----------------
       // (one base descriptor plus per-stage and per-slice offsets, see the prefill kernel)
       constexpr uint32_t idesc = idesc_f16_f32(2 * kBM, BN);
@@ -210,25 +211,29 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
       int s = 0;
       for (int i = 0; i < nK && ok; ++i) {
         ok = mbar_wait(&afull[i % kS2], (i / kS2) & 1, p.status, p.wait_limit);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t ds = dbase + (uint64_t)((s * L::kBytes) >> 4);
-        const uint32_t at = tmem + BN + 64 * (i % kS2);
-        if (i < nD) {
-          mma_f16_ts_pair(tmem, at, ds, idesc, i != 0);
-          #pragma unroll
-          for (int kk = 1; kk < 8; ++kk)
-            mma_f16_ts_pair(tmem, at + 8 * kk, ds + (uint64_t)((((kk >> 2) * BN * 64) + (kk & 3) * 32) >> 4), idesc, 1u);
-        } else {   // only the slices that hold weak columns
-          #pragma unroll 1
-          for (int kk = 0; kk < 8; ++kk)
-            if ((i - nD) * 64 + (kk & 3) * 16 < p.k_ld[kk >> 2])
+        if (elect_one()) {
+          const uint64_t ds = dbase + (uint64_t)((s * L::kBytes) >> 4);
+          const uint32_t at = tmem + BN + 64 * (i % kS2);
+          if (i < nD) {
+            mma_f16_ts_pair(tmem, at, ds, idesc, i != 0);
+            #pragma unroll
+            for (int kk = 1; kk < 8; ++kk)
               mma_f16_ts_pair(tmem, at + 8 * kk, ds + (uint64_t)((((kk >> 2) * BN * 64) + (kk & 3) * 32) >> 4), idesc, 1u);
+          } else {   // only the slices that hold weak columns
+            #pragma unroll 1
+            for (int kk = 0; kk < 8; ++kk)
+              if ((i - nD) * 64 + (kk & 3) * 16 < p.k_ld[kk >> 2])
+                mma_f16_ts_pair(tmem, at + 8 * kk, ds + (uint64_t)((((kk >> 2) * BN * 64) + (kk & 3) * 32) >> 4), idesc, 1u);
+          }
+          mma_commit_pair(&empty[s]);
         }
-        mma_commit_pair(&empty[s]);
+        __syncwarp();
         if (++s == S) s = 0;
       }
-      mma_commit_pair(accf);
+      if (elect_one()) mma_commit_pair(accf);
     }
   } else {
     // ---------------- A operand ----------------
@@ -302,12 +307,23 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
     }
 
     // ---------------- epilogue ----------------
-    const bool acc_ok = __all_sync(0xffffffffu, mbar_wait(accf, 0, p.status, p.wait_limit) && ok);
-    tc_fence_after();
     constexpr int kCols = BN / (kDW / 4);   // accumulator columns of this warp
     const int col0 = (aw >> 2) * kCols;
-    #pragma unroll 1
-    for (int c0 = col0; c0 < col0 + kCols; c0 += 16) {
+    // this lane finishes columns 8 lay .. 8 lay + 7 of every 16; in the backward pass their
+    // gradients are fetched while the last MMAs run
+    __half dhv[kCols / 2];
+    if (p.dh != nullptr && to.n_splits == 1) {
+      #pragma unroll
+      for (int e = 0; e < kCols / 2; ++e) {
+        const int t = m0 + col0 + (e / 8) * 16 + 8 * lay + e % 8;
+        dhv[e] = t < p.M && orow < p.N ? p.dh[(size_t)t * p.N + orow] : __float2half_rn(0.f);
+      }
+    }
+    const bool acc_ok = __all_sync(0xffffffffu, mbar_wait(accf, 0, p.status, p.wait_limit) && ok);
+    tc_fence_after();
+    #pragma unroll
+    for (int c = 0; c < kCols; c += 16) {
+      const int c0 = col0 + c;
       uint32_t v[16];
       tmem_ld16(tmem + lane_base + (uint32_t)c0, v);
       tmem_ld_wait();
@@ -323,7 +339,7 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
           const uint32_t got = __shfl_xor_sync(0xffffffffu, lay ? v[j] : v[j + 8], 16);
           const float gs = __uint_as_float(lay ? got : v[j]), us = __uint_as_float(lay ? v[j + 8] : got);
           const int t = m0 + c0 + j + 8 * lay;
-          if (t < p.M && orow < p.N) gated_store(p, (size_t)t * p.N + orow, gs, us);
+          if (t < p.M && orow < p.N) gated_store(p, (size_t)t * p.N + orow, gs, us, dhv[c / 2 + j]);
         }
       }
     }
@@ -372,7 +388,8 @@ __global__ void k_gated_reduce(const __grid_constant__ GatedGemmParams p, int BN
       gs += w[z * stride];
       us += w[z * stride + 16];
     }
-    gated_store(p, (size_t)t * p.N + row, gs, us);
+    const size_t o = (size_t)t * p.N + row;
+    gated_store(p, o, gs, us, p.dh ? p.dh[o] : __float2half_rn(0.f));
   }
 }
 
@@ -462,7 +479,7 @@ template <int BITS, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(32 * (2 + kDW), 1)
 k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ GatedIgParams p) {
   using L = Stage<BITS, BN>;
-  constexpr int S = L::kS;
+  constexpr int S = L::kS, kS2 = a_stages<BN>();
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * L::kBytes);
@@ -472,7 +489,7 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
   uint64_t* accf = bars + 2 * S + kS2;   // accumulator complete
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + kS2 + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (warp: uniform)
   const int rank = (int)cluster_ctarank();
   const int Kb = p.K / kStepCodes, Kp = (Kb + 1) / 2;   // column blocks, and pairs of them
   const int nR = (p.N + 127) / 128;     // row steps of one layer
@@ -528,7 +545,7 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
         mbar_wait(&full[i % S], (i / S) & 1, p.status, p.wait_limit);
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {   // the whole warp runs the loop, so that its values stay in uniform registers
       // ---------------- MMA issuer ----------------
       // (one base descriptor plus per-stage and per-slice offsets, see the prefill kernel)
       constexpr uint32_t idesc = idesc_f16_f32(2 * kBM, BN);
@@ -537,18 +554,22 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
       int s = 0;
       for (int i = 0; i < nK && ok; ++i) {
         ok = mbar_wait(&afull[i % kS2], (i / kS2) & 1, p.status, p.wait_limit);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t ds = dbase + (uint64_t)((s * L::kBytes) >> 4);
-        const uint32_t at = tmem + BN + 64 * (i % kS2);
-        mma_f16_ts_pair(tmem, at, ds, idesc, i != 0);
-        #pragma unroll
-        for (int kk = 1; kk < 8; ++kk)
-          mma_f16_ts_pair(tmem, at + 8 * kk, ds + (uint64_t)((((kk >> 2) * BN * 64) + (kk & 3) * 32) >> 4), idesc, 1u);
-        mma_commit_pair(&empty[s]);
+        if (elect_one()) {
+          const uint64_t ds = dbase + (uint64_t)((s * L::kBytes) >> 4);
+          const uint32_t at = tmem + BN + 64 * (i % kS2);
+          mma_f16_ts_pair(tmem, at, ds, idesc, i != 0);
+          #pragma unroll
+          for (int kk = 1; kk < 8; ++kk)
+            mma_f16_ts_pair(tmem, at + 8 * kk, ds + (uint64_t)((((kk >> 2) * BN * 64) + (kk & 3) * 32) >> 4), idesc, 1u);
+          mma_commit_pair(&empty[s]);
+        }
+        __syncwarp();
         if (++s == S) s = 0;
       }
-      mma_commit_pair(accf);
+      if (elect_one()) mma_commit_pair(accf);
     }
   } else {
     // ---------------- A operand: W_hat^T ----------------
@@ -900,8 +921,8 @@ owq_status_t run_gemm(const Layer& gate, const Layer& up, int act, const __half*
   auto kern = k_gated_gemm<BITS, BN>;
   constexpr int smem = ring_smem_bytes<BITS, BN>();
   static_assert(smem <= 232448 && 2 * smem > 232448, "one CTA per SM: the tensor memory of one");
-  static_assert(BN + 64 * kS2 <= (int)kTmemCols, "tensor memory: accumulator + A stages");
-  static_assert(Stage<BITS, BN>::kS >= kS2, "an A stage's MMAs are waited for on the ring's barriers");
+  static_assert(BN + 64 * a_stages<BN>() <= (int)kTmemCols, "tensor memory: accumulator + A stages");
+  static_assert(Stage<BITS, BN>::kS >= a_stages<BN>(), "an A stage's MMAs are waited for on the ring's barriers");
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
     cudaGetLastError();
     return OWQ_ERR_CUDA;
