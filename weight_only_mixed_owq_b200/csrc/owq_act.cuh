@@ -9,6 +9,8 @@
 // 2^-22 + |x| 2^-24 and 2^-23: far inside the outputs' fp16 rounding of 2^-11); with the
 // correctly rounded ones the epilogue of a 256-token tile took 3 us more.
 #pragma once
+#include <type_traits>
+
 #include "owq_internal.cuh"
 
 namespace owq {
@@ -33,17 +35,14 @@ __device__ __forceinline__ void act_eval(float g, float& a, float& da) {
     da = s + g * (s * (1.f - s)) * (2.f * c * (1.f + 3.f * k * g2));
   }
 }
-__device__ __forceinline__ float act_value(int act, float g) {
-  float a, da;
-  if (act == OWQ_ACT_SILU) act_eval<OWQ_ACT_SILU>(g, a, da);
-  else if (act == OWQ_ACT_GELU) act_eval<OWQ_ACT_GELU>(g, a, da);
-  else act_eval<OWQ_ACT_GELU_TANH>(g, a, da);
-  return a;
-}
-__device__ __forceinline__ void act_both(int act, float g, float& a, float& da) {
-  if (act == OWQ_ACT_SILU) act_eval<OWQ_ACT_SILU>(g, a, da);
-  else if (act == OWQ_ACT_GELU) act_eval<OWQ_ACT_GELU>(g, a, da);
-  else act_eval<OWQ_ACT_GELU_TANH>(g, a, da);
+// f(std::integral_constant<int, act>): one copy of the code around an activation per kind, so that
+// no element branches on it (inlined in every element of an unrolled epilogue, the three forms
+// were more code than the instruction cache holds).
+template <class F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  if (act == OWQ_ACT_SILU) f(std::integral_constant<int, OWQ_ACT_SILU>{});
+  else if (act == OWQ_ACT_GELU) f(std::integral_constant<int, OWQ_ACT_GELU>{});
+  else f(std::integral_constant<int, OWQ_ACT_GELU_TANH>{});
 }
 
 }  // namespace owq

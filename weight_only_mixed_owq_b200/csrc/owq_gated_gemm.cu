@@ -96,16 +96,51 @@ struct GatedGemmParams {
   int skip_arrive;
 };
 
-// outputs of one element; gs, us: both projections; dhv: its gradient (backward)
+// outputs of one element; gs, us: both projections; dhv: its gradient (BWD)
+template <int ACT, bool BWD>
 __device__ __forceinline__ void gated_store(const GatedGemmParams& p, size_t o, float gs, float us, __half dhv) {
-  if (p.dh == nullptr) {
-    p.out[0][o] = __float2half_rn(act_value(p.act, gs) * us);
-  } else {
-    float a, da;
-    act_both(p.act, gs, a, da);
+  float a, da;
+  act_eval<ACT>(gs, a, da);
+  if constexpr (BWD) {
     const float dh = __half2float(dhv);
     p.out[0][o] = __float2half_rn(dh * us * da);
     p.out[1][o] = __float2half_rn(dh * a);
+  } else {
+    p.out[0][o] = __float2half_rn(a * us);
+  }
+}
+
+// Epilogue of a whole tile: lanes l (gate row) and l + 16 (the up row of the same output) exchange
+// halves; a gate lane finishes columns (tokens) 0-7 of every 16, the up lane 8-15.  `acc`: this
+// warp's first column in tensor memory, `first`: its token for this lane, `o`: that output.  The
+// backward pass fetches 8 gradients ahead, the first before the accumulator is waited for.
+template <int ACT, bool BWD, int COLS, class Wait>
+__device__ __forceinline__ void gated_epilogue(const GatedGemmParams& p, uint32_t acc, int first, int orow, int lay, Wait&& wait) {
+  const bool row_ok = orow < p.N;
+  size_t o = (size_t)first * p.N + orow;
+  __half next[8];
+  auto fetch = [&](int c) {
+    #pragma unroll
+    for (int j = 0; j < 8; ++j)
+      next[j] = BWD && row_ok && first + c + j < p.M ? p.dh[o + (size_t)(c + j) * p.N] : __float2half_rn(0.f);
+  };
+  fetch(0);
+  if (!wait()) return;
+  #pragma unroll 1
+  for (int c = 0; c < COLS; c += 16) {
+    uint32_t v[16];
+    tmem_ld16(acc + (uint32_t)c, v);
+    __half dhv[8];
+    #pragma unroll
+    for (int j = 0; j < 8; ++j) dhv[j] = next[j];
+    if (BWD && c + 16 < COLS) fetch(c + 16);
+    tmem_ld_wait();
+    #pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, lay ? v[j] : v[j + 8], 16);
+      const float gs = __uint_as_float(lay ? got : v[j]), us = __uint_as_float(lay ? v[j + 8] : got);
+      if (row_ok && first + c + j < p.M) gated_store<ACT, BWD>(p, o + (size_t)(c + j) * p.N, gs, us, dhv[j]);
+    }
   }
 }
 
@@ -309,39 +344,30 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
     // ---------------- epilogue ----------------
     constexpr int kCols = BN / (kDW / 4);   // accumulator columns of this warp
     const int col0 = (aw >> 2) * kCols;
-    // this lane finishes columns 8 lay .. 8 lay + 7 of every 16; in the backward pass their
-    // gradients are fetched while the last MMAs run
-    __half dhv[kCols / 2];
-    if (p.dh != nullptr && to.n_splits == 1) {
-      #pragma unroll
-      for (int e = 0; e < kCols / 2; ++e) {
-        const int t = m0 + col0 + (e / 8) * 16 + 8 * lay + e % 8;
-        dhv[e] = t < p.M && orow < p.N ? p.dh[(size_t)t * p.N + orow] : __float2half_rn(0.f);
-      }
-    }
-    const bool acc_ok = __all_sync(0xffffffffu, mbar_wait(accf, 0, p.status, p.wait_limit) && ok);
-    tc_fence_after();
-    #pragma unroll
-    for (int c = 0; c < kCols; c += 16) {
-      const int c0 = col0 + c;
-      uint32_t v[16];
-      tmem_ld16(tmem + lane_base + (uint32_t)c0, v);
-      tmem_ld_wait();
-      if (!acc_ok) continue;
-      if (to.n_splits > 1) {   // this split's fp32 partials
-        float* w = p.ws + partial_at(p.split, to.split, to.tile, rank, BN) + (size_t)c0 * kBM + 32 * quarter + lane;
+    const uint32_t acc = tmem + lane_base + (uint32_t)col0;
+    auto wait = [&]() {
+      const bool acc_ok = __all_sync(0xffffffffu, mbar_wait(accf, 0, p.status, p.wait_limit) && ok);
+      tc_fence_after();
+      return acc_ok;
+    };
+    if (to.n_splits > 1) {   // this split's fp32 partials
+      const bool acc_ok = wait();
+      float* w = p.ws + partial_at(p.split, to.split, to.tile, rank, BN) + (size_t)col0 * kBM + 32 * quarter + lane;
+      #pragma unroll 1
+      for (int c = 0; c < kCols && acc_ok; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(acc + (uint32_t)c, v);
+        tmem_ld_wait();
         #pragma unroll
-        for (int j = 0; j < 16; ++j) w[j * kBM] = __uint_as_float(v[j]);
-      } else {
-        // a gate lane finishes columns 0-7, the up lane of the same output columns 8-15
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t got = __shfl_xor_sync(0xffffffffu, lay ? v[j] : v[j + 8], 16);
-          const float gs = __uint_as_float(lay ? got : v[j]), us = __uint_as_float(lay ? v[j + 8] : got);
-          const int t = m0 + c0 + j + 8 * lay;
-          if (t < p.M && orow < p.N) gated_store(p, (size_t)t * p.N + orow, gs, us, dhv[c / 2 + j]);
-        }
+        for (int j = 0; j < 16; ++j) w[(size_t)(c + j) * kBM] = __uint_as_float(v[j]);
       }
+    } else {
+      with_act(p.act, [&](auto act) {
+        constexpr int A = decltype(act)::value;
+        const int first = m0 + col0 + 8 * lay;
+        if (p.dh) gated_epilogue<A, true, kCols>(p, acc, first, orow, lay, wait);
+        else gated_epilogue<A, false, kCols>(p, acc, first, orow, lay, wait);
+      });
     }
   }
 
@@ -389,7 +415,11 @@ __global__ void k_gated_reduce(const __grid_constant__ GatedGemmParams p, int BN
       us += w[z * stride + 16];
     }
     const size_t o = (size_t)t * p.N + row;
-    gated_store(p, o, gs, us, p.dh ? p.dh[o] : __float2half_rn(0.f));
+    with_act(p.act, [&](auto act) {
+      constexpr int A = decltype(act)::value;
+      if (p.dh) gated_store<A, true>(p, o, gs, us, p.dh[o]);
+      else gated_store<A, false>(p, o, gs, us, __float2half_rn(0.f));
+    });
   }
 }
 

@@ -350,7 +350,11 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
       gs += src[row * MT + m];
       us += src[(16 + row) * MT + m];
     }
-    a.h[(size_t)m * a.N + n] = __float2half_rn(act_value(a.act, gs) * us);
+    with_act(a.act, [&](auto act) {
+      float v, dv;
+      act_eval<decltype(act)::value>(gs, v, dv);
+      a.h[(size_t)m * a.N + n] = __float2half_rn(v * us);
+    });
   }
 }
 
