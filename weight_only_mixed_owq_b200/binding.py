@@ -406,15 +406,22 @@ def _check_tensor(t, name: str, shape, dtype, device=None) -> None:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
 
 
-def _run_on(device, stream, fn):
+def _raw_stream(torch, index: int) -> int:
+    """The current stream's handle on device `index` (torch.cuda.current_stream builds an object
+    for it, which costs more than a launch)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _run_on(torch, device, stream, fn):
     """fn(stream handle) with `device` current and, for an explicit stream (a torch stream or a
     raw handle), that stream current too, so that what fn allocates belongs to it."""
-    import torch
-    if torch.cuda.current_device() != device.index:
+    index = device.index
+    if torch.cuda.current_device() != index:
         with torch.cuda.device(device):
-            return _run_on(device, stream, fn)
+            return _run_on(torch, device, stream, fn)
     if stream is None:
-        return fn(torch.cuda.current_stream().cuda_stream)
+        return fn(_raw_stream(torch, index))
     ext = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
     with torch.cuda.stream(ext):
         return fn(ext.cuda_stream)
@@ -429,6 +436,7 @@ class OwqGated:
     ACTS = {"silu": OWQ_ACT_SILU, "gelu": OWQ_ACT_GELU, "gelu_tanh": OWQ_ACT_GELU_TANH}
 
     def __init__(self, gate: OwqLayer, up: OwqLayer, act: str = "silu"):
+        import torch
         if act not in self.ACTS:
             raise ValueError(f"act {act!r}: expected one of {sorted(self.ACTS)}")
         for what in ("N", "K", "bits", "group"):
@@ -436,26 +444,26 @@ class OwqGated:
                 raise ValueError(f"gate and up differ in {what}: {getattr(gate, what)} and {getattr(up, what)}")
         self.gate, self.up, self.act = gate, up, self.ACTS[act]
         self.N, self.K = gate.N, gate.K
+        self._torch, self._half = torch, torch.float16
 
     def _rows(self, t, name: str, width: int) -> int:
-        import torch
         if t.dim() != 2:
             raise ValueError(f"{name}: expected 2 dimensions, got {tuple(t.shape)}")
-        _check_tensor(t, name, (t.shape[0], width), torch.float16)
-        return t.shape[0]
+        M = t.shape[0]
+        if t.dtype != self._half or t.shape[1] != width or not t.is_cuda or not t.is_contiguous():
+            _check_tensor(t, name, (M, width), self._half)
+        return M
 
     def _out(self, t, name: str, M: int, width: int, like):
-        import torch
         if t is None:
-            return torch.empty((M, width), dtype=torch.float16, device=like.device)
-        _check_tensor(t, name, (M, width), torch.float16, like.device)
+            return like.new_empty((M, width))
+        _check_tensor(t, name, (M, width), self._half, like.device)
         return t
 
-    def _workspace(self, M: int, device):
-        import torch
+    def _workspace(self, M: int, like):
         st, n = owq_gated_workspace(self.gate.handle, self.up.handle, M)
         _check(st, "owq_gated_workspace")
-        return torch.empty(n, dtype=torch.uint8, device=device), n
+        return like.new_empty((n,), dtype=self._torch.uint8), n
 
     def gemv(self, x, h=None, stream=None):
         """h for 1 to 16 tokens (x: M x K)."""
@@ -466,53 +474,56 @@ class OwqGated:
             _check(LIB.owq_gated_gemv(self.gate.handle, self.up.handle, self.act, x.data_ptr(), y.data_ptr(), M, s),
                    "owq_gated_gemv")
             return y
-        return _run_on(x.device, stream, go)
+        return _run_on(self._torch, x.device, stream, go)
 
     def gemm(self, x, h=None, stream=None):
         """h for any number of tokens (tuned for 64 and more)."""
         M = self._rows(x, "x", self.K)
 
         def go(s):
-            ws, n = self._workspace(M, x.device)
+            ws, n = self._workspace(M, x)
             y = self._out(h, "h", M, self.N, x)
-            _check(owq_gated_gemm(self.gate.handle, self.up.handle, self.act, x, y, M, ws, n, s), "owq_gated_gemm")
+            _check(LIB.owq_gated_gemm(self.gate.handle, self.up.handle, self.act, x.data_ptr(), y.data_ptr(), M, ws.data_ptr(), n, s),
+                   "owq_gated_gemm")
             return y
-        return _run_on(x.device, stream, go)
+        return _run_on(self._torch, x.device, stream, go)
+
+    def _grad(self, x, dh, dgate, dup, M, ws, n, s):
+        g, u = self._out(dgate, "dgate", M, self.N, x), self._out(dup, "dup", M, self.N, x)
+        _check(LIB.owq_gated_grad(self.gate.handle, self.up.handle, self.act, x.data_ptr(), dh.data_ptr(), g.data_ptr(),
+                                  u.data_ptr(), M, ws.data_ptr(), n, s), "owq_gated_grad")
+        return g, u
+
+    def _input_grad(self, dgate, dup, dx, M, ws, n, s):
+        d = self._out(dx, "dx", M, self.K, dgate)
+        _check(LIB.owq_gated_input_grad(self.gate.handle, self.up.handle, dgate.data_ptr(), dup.data_ptr(), d.data_ptr(), M,
+                                        ws.data_ptr(), n, s), "owq_gated_input_grad")
+        return d
 
     def grad(self, x, dh, dgate=None, dup=None, stream=None):
         """(dgate, dup): the gradients of x Wg^T and x Wu^T, recomputed from x."""
         M = self._rows(x, "x", self.K)
-        _check_fp16(dh, "dh", (M, self.N), x.device)
-
-        def go(s):
-            ws, n = self._workspace(M, x.device)
-            g, u = self._out(dgate, "dgate", M, self.N, x), self._out(dup, "dup", M, self.N, x)
-            _check(owq_gated_grad(self.gate.handle, self.up.handle, self.act, x, dh, g, u, M, ws, n, s), "owq_gated_grad")
-            return g, u
-        return _run_on(x.device, stream, go)
+        _check_tensor(dh, "dh", (M, self.N), self._half, x.device)
+        return _run_on(self._torch, x.device, stream, lambda s: self._grad(x, dh, dgate, dup, M, *self._workspace(M, x), s))
 
     def input_grad(self, dgate, dup, dx=None, stream=None):
         """dx = dgate Wg + dup Wu."""
         M = self._rows(dgate, "dgate", self.N)
-        _check_fp16(dup, "dup", (M, self.N), dgate.device)
-
-        def go(s):
-            ws, n = self._workspace(M, dgate.device)
-            d = self._out(dx, "dx", M, self.K, dgate)
-            _check(owq_gated_input_grad(self.gate.handle, self.up.handle, dgate, dup, d, M, ws, n, s), "owq_gated_input_grad")
-            return d
-        return _run_on(dgate.device, stream, go)
+        _check_tensor(dup, "dup", (M, self.N), self._half, dgate.device)
+        return _run_on(self._torch, dgate.device, stream,
+                       lambda s: self._input_grad(dgate, dup, dx, M, *self._workspace(M, dgate), s))
 
     def backward(self, x, dh, dx=None, dgate=None, dup=None, stream=None):
         """(dx, dgate, dup) from the gradient dh of h.  The weak blocks' gradients follow with
         gate.weak_grad(x, dgate) and up.weak_grad(x, dup)."""
-        g, u = self.grad(x, dh, dgate, dup, stream)
-        return self.input_grad(g, u, dx, stream), g, u
+        M = self._rows(x, "x", self.K)
+        _check_tensor(dh, "dh", (M, self.N), self._half, x.device)
 
-
-def _check_fp16(t, name: str, shape, device) -> None:
-    import torch
-    _check_tensor(t, name, shape, torch.float16, device)
+        def go(s):
+            ws, n = self._workspace(M, x)
+            g, u = self._grad(x, dh, dgate, dup, M, ws, n, s)
+            return self._input_grad(g, u, dx, M, ws, n, s), g, u
+        return _run_on(self._torch, x.device, stream, go)
 
 
 class OwqGradClip:
@@ -523,6 +534,7 @@ class OwqGradClip:
     def __init__(self, grads, outs=None, stream=None):
         import torch
         self.handle = None
+        self._torch = torch
         self.grads = list(grads)
         self.outs = self.grads if outs is None else list(outs)
         kinds = {torch.float32: OWQ_F32, torch.float16: OWQ_F16, torch.bfloat16: OWQ_BF16}
@@ -537,18 +549,19 @@ class OwqGradClip:
             if o is not g:
                 _check_tensor(o, f"output {i}", g.shape, g.dtype, self.device)
             table[i] = OwqGrad(g.data_ptr(), o.data_ptr(), g.numel(), kinds[g.dtype])
-        st, self.handle = _run_on(self.device, stream, lambda s: owq_clip_create(table, len(self.grads), s))
+        st, self.handle = _run_on(torch, self.device, stream, lambda s: owq_clip_create(table, len(self.grads), s))
         _check(st, "owq_clip_create")
 
     def __call__(self, max_norm: float, norm=None, stream=None):
-        import torch
+        torch = self._torch
 
         def go(s):
             n = torch.empty(1, dtype=torch.float32, device=self.device) if norm is None else norm
-            _check_tensor(n, "norm", (1,), torch.float32, self.device)
-            _check(owq_clip_grads(self.handle, max_norm, n, s), "owq_clip_grads")
+            if norm is not None:
+                _check_tensor(n, "norm", (1,), torch.float32, self.device)
+            _check(LIB.owq_clip_grads(self.handle, max_norm, n.data_ptr(), s), "owq_clip_grads")
             return n
-        return _run_on(self.device, stream, go)
+        return _run_on(torch, self.device, stream, go)
 
     def close(self):
         if getattr(self, "handle", None):

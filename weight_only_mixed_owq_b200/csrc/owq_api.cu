@@ -1,7 +1,6 @@
 // C ABI of the library (declared in include/owq.h): argument validation, layer handles,
 // launches.  Every argument is validated on the host before anything is launched.
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -34,6 +33,14 @@ int layer_sm_count(int dev) {
     n[dev].store(v, std::memory_order_relaxed);
   }
   return v;
+}
+
+cudaError_t allow_smem(const void* kern, int bytes, int dev, std::atomic<unsigned long long>& done) {
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 namespace {
@@ -284,6 +291,8 @@ owq_status_t owq_pack(const uint8_t* codes, int N, int K, int bits, int group, c
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);  // host tables above must outlive the copies
   cudaFree(mask_dev);
   if (e != cudaSuccess) { release(L); return cuda_status(e); }
+  L->status = device_status_ptr();
+  if (!L->status || !encode_gated_maps(*L)) { release(L); return OWQ_ERR_CUDA; }
   {
     std::lock_guard<std::mutex> g(g_mu);
     registry().insert(L);
@@ -666,6 +675,8 @@ owq_status_t owq_clip_create(const owq_grad_t* grads, int count, owq_stream_t st
   c->part = nullptr;
   const int sms = layer_sm_count(c->device);
   c->chunk_bytes = clip_chunk_bytes(total, sms);
+  c->status = device_status_ptr();
+  if (!c->status) { delete c; return OWQ_ERR_CUDA; }
   std::vector<ClipChunk> table;
   for (int i = 0; i < count; ++i) {
     const owq_grad_t& t = grads[i];

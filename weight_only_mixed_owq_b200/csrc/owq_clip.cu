@@ -223,13 +223,13 @@ cudaError_t launch_clip(const Clip& c, float max_norm, float* norm, long long wa
   a.arrived = c.arrived;
   a.max_norm = max_norm;
   a.norm = norm;
-  a.status = device_status_ptr();
+  a.status = c.status;
   a.wait_limit = wait_limit;
-  if (!a.status) return cudaErrorInvalidDevicePointer;
   const int per = (c.n_chunks + c.grid - 1) / c.grid;
   a.cached = std::min(per, kCacheBytes / c.chunk_bytes);
   const int smem = a.cached * c.chunk_bytes;
-  cudaError_t e = cudaFuncSetAttribute(k_clip, cudaFuncAttributeMaxDynamicSharedMemorySize, kCacheBytes);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_smem((const void*)k_clip, kCacheBytes, c.device, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(c.grid);
@@ -241,7 +241,9 @@ cudaError_t launch_clip(const Clip& c, float max_norm, float* norm, long long wa
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_clip, a);
+  e = cudaLaunchKernelEx(&cfg, k_clip, a);
+  if (e != cudaSuccess) allowed = 0;
+  return e;
 }
 
 }  // namespace owq

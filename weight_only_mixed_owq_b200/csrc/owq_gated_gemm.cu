@@ -929,19 +929,18 @@ owq_status_t run_gemm(const Layer& gate, const Layer& up, int act, const __half*
     ga.xw[l] = reinterpret_cast<__half*>(ws + f.xw[l]);
     ga.k[l] = L[l]->k;
     ga.k_ld[l] = prm.k_ld[l];
-    if (!encode_packed_3d(&maps.p[l], L[l]->packed, L[l]->K, L[l]->N, BITS, kHalfRows / 16) ||
-        !encode_sz_3d(&maps.sz[l], L[l]->sz_t, L[l]->G, L[l]->N, kHalfRows / 16) ||
-        // (a layer without weak columns: x itself, loaded and never multiplied)
-        !encode_2d(&maps.xw[l], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, L[l]->k > 0 ? ga.xw[l] : x,
-                   (uint64_t)(L[l]->k > 0 ? L[l]->k_ld : gate.K), (uint64_t)M, (uint64_t)(L[l]->k > 0 ? L[l]->k_ld : gate.K) * 2, 64,
-                   BN / 2, CU_TENSOR_MAP_SWIZZLE_128B))
+    maps.p[l] = L[l]->gated_p[0];
+    maps.sz[l] = L[l]->gated_sz[0];
+    maps.xw[l] = maps.x;   // (a layer without weak columns: x itself, loaded and never multiplied)
+    if (L[l]->k > 0 &&
+        !encode_2d(&maps.xw[l], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ga.xw[l], (uint64_t)L[l]->k_ld, (uint64_t)M, (uint64_t)L[l]->k_ld * 2,
+                   64, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B))
       return OWQ_ERR_CUDA;
   }
   prm.dh = dh;
   prm.out[0] = out0;
   prm.out[1] = out1;
-  prm.status = device_status_ptr();
-  if (!prm.status) return OWQ_ERR_CUDA;
+  prm.status = gate.status;
   prm.N = gate.N; prm.K = gate.K; prm.M = M; prm.G = gate.G; prm.act = act;
   prm.wait_limit = wait_limit; prm.skip_arrive = skip_arrive ? 1 : 0;
   prm.nw = (std::max(prm.k_ld[0], prm.k_ld[1]) + 63) / 64;
@@ -953,7 +952,8 @@ owq_status_t run_gemm(const Layer& gate, const Layer& up, int act, const __half*
   static_assert(smem <= 232448 && 2 * smem > 232448, "one CTA per SM: the tensor memory of one");
   static_assert(BN + 64 * a_stages<BN>() <= (int)kTmemCols, "tensor memory: accumulator + A stages");
   static_assert(Stage<BITS, BN>::kS >= a_stages<BN>(), "an A stage's MMAs are waited for on the ring's barriers");
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+  static std::atomic<unsigned long long> allowed{0};
+  if (allow_smem((const void*)kern, smem, gate.device, allowed) != cudaSuccess) {
     cudaGetLastError();
     return OWQ_ERR_CUDA;
   }
@@ -966,6 +966,7 @@ owq_status_t run_gemm(const Layer& gate, const Layer& up, int act, const __half*
   void* args[] = {&maps, &prm};
   if (launch_pdl((void*)kern, dim3(2 * f.split.pairs()), 32 * (2 + kDW), smem, ld > 0, s, args) != cudaSuccess) {
     cudaGetLastError();
+    allowed = 0;
     return OWQ_ERR_CUDA;
   }
   if (f.split.splits > 1) {
@@ -1044,10 +1045,10 @@ owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const 
   const int Kb = gate.K / kStepCodes;
   for (int l = 0; l < 2; ++l) {
     if (!encode_2d(&maps.dy[l], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dy[l], (uint64_t)gate.N, (uint64_t)M, (uint64_t)f.ldy * 2, 64, BN / 2,
-                   CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_packed_3d(&maps.p[l], L[l]->packed, L[l]->K, L[l]->N, BITS) ||
-        !encode_sz_3d(&maps.sz[l], L[l]->sz_t, L[l]->G, L[l]->N))
+                   CU_TENSOR_MAP_SWIZZLE_128B))
       return OWQ_ERR_CUDA;
+    maps.p[l] = L[l]->gated_p[1];
+    maps.sz[l] = L[l]->gated_sz[1];
     prm.wk[l] = wa.wk[l] = reinterpret_cast<float*>(ws + f.wk[l]);
     prm.idx[l] = L[l]->idx;
     prm.k[l] = wa.k[l] = L[l]->k;
@@ -1059,8 +1060,7 @@ owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const 
   if (!encode_2d(&maps.dx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dx, (uint64_t)gate.K, (uint64_t)M, (uint64_t)gate.K * 2, kStepCodes, BN,
                  CU_TENSOR_MAP_SWIZZLE_NONE))
     return OWQ_ERR_CUDA;
-  prm.status = device_status_ptr();
-  if (!prm.status) return OWQ_ERR_CUDA;
+  prm.status = gate.status;
   prm.N = gate.N; prm.K = gate.K; prm.M = M; prm.group = gate.group;
   prm.split = f.split;
   prm.wait_limit = wait_limit;
@@ -1072,7 +1072,8 @@ owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const 
   auto kern = k_gated_igemm<BITS, BN>;
   constexpr int smem = ring_smem_bytes<BITS, BN>();
   static_assert(BN * kStepCodes * 2 <= Stage<BITS, BN>::kS * Stage<BITS, BN>::kBytes, "output tile in the stages");
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+  static std::atomic<unsigned long long> allowed{0};
+  if (allow_smem((const void*)kern, smem, gate.device, allowed) != cudaSuccess) {
     cudaGetLastError();
     return OWQ_ERR_CUDA;
   }
@@ -1086,6 +1087,7 @@ owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const 
   void* args[] = {&maps, &prm};
   if (launch_pdl((void*)kern, dim3(2 * f.split.pairs()), 32 * (2 + kDW), smem, C > 0, s, args) != cudaSuccess) {
     cudaGetLastError();
+    allowed = 0;
     return OWQ_ERR_CUDA;
   }
   if (f.split.splits > 1) {
@@ -1111,6 +1113,15 @@ owq_status_t dispatch_ig(const Layer& gate, const Layer& up, const __half* dg, c
 }
 
 }  // namespace
+
+bool encode_gated_maps(Layer& L) {
+  for (int i = 0; i < 2; ++i) {
+    const int tiles = (i + 1) * kHalfRows / 16;
+    if (!encode_packed_3d(&L.gated_p[i], L.packed, L.K, L.N, L.bits, tiles) || !encode_sz_3d(&L.gated_sz[i], L.sz_t, L.G, L.N, tiles))
+      return false;
+  }
+  return true;
+}
 
 size_t gated_gemm_ws_bytes(const Layer& gate, const Layer& up, int M) { return fwd_plan(gate, up, M).total; }
 size_t gated_input_grad_ws_bytes(const Layer& gate, const Layer& up, int M) { return ig_plan(gate, up, M).total; }

@@ -359,14 +359,15 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
 }
 
 template <int BITS, int NT, bool PG>
-cudaError_t launch_p(GatedGemvArgs& a, int grid, cudaStream_t s) {
+cudaError_t launch_p(GatedGemvArgs& a, int grid, int dev, cudaStream_t s) {
   a.wunits = (std::max(a.nsl[0], a.nsl[1]) + Unit<BITS>::kSlices - 1) / Unit<BITS>::kSlices;
   a.tcap = (a.tiles + grid - 1) / grid;
   // the largest items and deepest rings that fit beside the activations; a ring of at least two
   // stages comes before keeping the activations in shared memory
   static constexpr int kShapes[][2] = {{4, 3}, {4, 2}, {2, 3}, {2, 2}, {1, 3}, {1, 2}};
+  static std::atomic<unsigned long long> allowed[2];   // [activations in shared memory]
   void (*kern)(GatedGemvArgs) = nullptr;
-  int smem = 0;
+  int smem = 0, in_smem = 0;
   for (int xs = 1; xs >= 0 && !kern; --xs)
     for (const auto& sh : kShapes) {
       const int total = smem_plan(stage_bytes<BITS>(sh[0], PG), sh[1], 8 * NT, a.tcap, PG, a.k[0], a.k[1], a.M, a.K, xs).total;
@@ -374,11 +375,12 @@ cudaError_t launch_p(GatedGemvArgs& a, int grid, cudaStream_t s) {
       a.sub = sh[0];
       a.stages = sh[1];
       smem = total;
+      in_smem = xs;
       kern = xs ? k_gated_gemv<BITS, NT, PG, true> : k_gated_gemv<BITS, NT, PG, false>;
       break;
     }
   if (!kern) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem((const void*)kern, kMaxSmem, dev, allowed[in_smem]);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -390,13 +392,15 @@ cudaError_t launch_p(GatedGemvArgs& a, int grid, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  e = cudaLaunchKernelEx(&cfg, kern, a);
+  if (e != cudaSuccess) allowed[in_smem] = 0;
+  return e;
 }
 
 template <int BITS>
-cudaError_t launch_b(GatedGemvArgs& a, bool pg, int grid, cudaStream_t s) {
-  if (a.M <= 8) return pg ? launch_p<BITS, 1, true>(a, grid, s) : launch_p<BITS, 1, false>(a, grid, s);
-  return pg ? launch_p<BITS, 2, true>(a, grid, s) : launch_p<BITS, 2, false>(a, grid, s);
+cudaError_t launch_b(GatedGemvArgs& a, bool pg, int grid, int dev, cudaStream_t s) {
+  if (a.M <= 8) return pg ? launch_p<BITS, 1, true>(a, grid, dev, s) : launch_p<BITS, 1, false>(a, grid, dev, s);
+  return pg ? launch_p<BITS, 2, true>(a, grid, dev, s) : launch_p<BITS, 2, false>(a, grid, dev, s);
 }
 
 }  // namespace
@@ -420,11 +424,10 @@ cudaError_t launch_gated_gemv(const Layer& gate, const Layer& up, int act, const
   a.M = M;
   a.act = act;
   a.tiles = (gate.N + 15) / 16;
-  a.status = device_status_ptr();
+  a.status = gate.status;
   a.wait_limit = wait_limit;
-  if (!a.status) return cudaErrorInvalidDevicePointer;
   const int grid = std::min(a.tiles, layer_sm_count(gate.device));
-  return gate.bits == 3 ? launch_b<3>(a, gate.G > 1, grid, s) : launch_b<4>(a, gate.G > 1, grid, s);
+  return gate.bits == 3 ? launch_b<3>(a, gate.G > 1, grid, gate.device, s) : launch_b<4>(a, gate.G > 1, grid, gate.device, s);
 }
 
 }  // namespace owq

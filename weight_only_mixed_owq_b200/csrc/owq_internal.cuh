@@ -4,6 +4,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <algorithm>
+#include <atomic>
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
 #include <cuda.h>
@@ -51,6 +52,10 @@ struct Layer {
   bool maps_ready;
   alignas(64) CUtensorMap map_packed;
   alignas(64) CUtensorMap map_sz;      // (scale, zero) pairs of per-group layers
+  // of the gated block, encoded at pack time: boxes of 4 and of 8 row tiles
+  alignas(64) CUtensorMap gated_p[2];
+  alignas(64) CUtensorMap gated_sz[2];
+  int* status;                         // the device status word
 };
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -182,6 +187,8 @@ owq_status_t gemm_sm100(Layer& L, const __half* x, __half* y, int M, long long w
                         bool skip_arrive, cudaStream_t s);
 
 // ---- gated block (two layers of one shape that share their input) ----
+// the layer's tensor maps for it (false: the driver refused one)
+bool encode_gated_maps(Layer& L);
 // decode form, M <= kMaxGemvM: one launch, no workspace
 cudaError_t launch_gated_gemv(const Layer& gate, const Layer& up, int act, const __half* x, __half* h, int M,
                               long long wait_limit, cudaStream_t s);
@@ -197,6 +204,9 @@ owq_status_t gated_input_grad_sm100(const Layer& gate, const Layer& up, const __
                                     void* ws, size_t ws_bytes, long long wait_limit, cudaStream_t s);
 // SM count of device `dev` (cached per device ordinal)
 int layer_sm_count(int dev);
+// Raise a kernel's dynamic shared memory limit, once per device (a bit of `done` each; the caller
+// clears it when a launch fails, so that the next call tries again).
+cudaError_t allow_smem(const void* kern, int bytes, int dev, std::atomic<unsigned long long>& done);
 
 // ---- gradient clipping ----
 struct ClipChunk {   // at most chunk_bytes / element size consecutive values of one tensor
@@ -208,6 +218,7 @@ struct Clip {
   int device;
   ClipChunk* chunks;             // device table
   int n_chunks, chunk_bytes, grid;
+  int* status;                   // the device status word
   double* part;                  // [grid] partial sums
   unsigned long long* arrived;   // CTAs that have published their sum, over all calls
 };
