@@ -70,13 +70,14 @@ def test_gemv(owq, shape, act):
     assert owq.owq_device_status() == 0
 
 
-@pytest.mark.parametrize("M", [1, 3, 13, 16])
-@pytest.mark.parametrize("bits", [3, 4])
-def test_gemv_long_rows(owq, bits, M):
-    """Rows so long that 13 and 16 tokens are read from global memory."""
-    shape = (40, 16384, bits, 128, 64, 100)
+# rows so long that the activations are split over clusters of 2, 4 and 8 CTAs, then that they are
+# read from global memory
+@pytest.mark.parametrize("bits,K,k,M", [(3, 5120, 40, 16), (4, 5120, 40, 12), (3, 16384, 64, 16), (4, 16384, 100, 1), (4, 16384, 100, 13),
+                                         (3, 36864, 288, 16), (4, 49152, 1024, 8), (4, 65536, 40, 16), (3, 65536, 0, 9)])
+def test_gemv_long_rows(owq, bits, K, k, M):
+    shape = (40, K, bits, 128, k, k)
     b, Wg, Wu = block(owq, *shape)
-    x = activations(M, M, shape[1])
+    x = activations(M, M, K)
     want, bound = ref.forward(x, Wg, Wu, "silu")
     ref.check(b.gemv(x), want, bound, f"{shape} M={M}")
 

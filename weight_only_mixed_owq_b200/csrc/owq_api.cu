@@ -269,6 +269,7 @@ owq_status_t owq_pack(const uint8_t* codes, int N, int K, int bits, int group, c
   std::vector<uint32_t> mask(K / 32, 0u);
   for (int t = 0; t < k; ++t) mask[hidx[t] / 32] |= 1u << (hidx[t] % 32);
   for (int b = 0; b < K / kBlockCodes; ++b) L->blk_weak[b] = 0u;
+  for (int t = 0; t < k; ++t) L->idx16[t] = (uint16_t)hidx[t];
   for (int t = k - 1; t >= 0; --t) {   // descending: the first slot of each block wins
     const int b = hidx[t] / kBlockCodes;
     L->blk_weak[b] = ((uint32_t)t << 16) | ((L->blk_weak[b] & 0xFFFFu) + 1u);

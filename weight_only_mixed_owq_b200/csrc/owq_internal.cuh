@@ -56,6 +56,7 @@ struct Layer {
   alignas(64) CUtensorMap gated_p[2];
   alignas(64) CUtensorMap gated_sz[2];
   int* status;                         // the device status word
+  uint16_t idx16[kMaxWeak];            // host copy of idx
 };
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
