@@ -71,11 +71,11 @@ def test_gemv(owq, shape, act):
 
 
 # rows so long that the activations are split over clusters of 2, 4 and 8 CTAs, then that they are
-# read from global memory
+# read from global memory; the last two have more tiles than one launch's sums
 @pytest.mark.parametrize("bits,K,k,M", [(3, 5120, 40, 16), (4, 5120, 40, 12), (3, 16384, 64, 16), (4, 16384, 100, 1), (4, 16384, 100, 13),
-                                         (3, 36864, 288, 16), (4, 49152, 1024, 8), (4, 65536, 40, 16), (3, 65536, 0, 9)])
+                                         (3, 36864, 288, 16), (4, 49152, 1024, 8), (4, 65536, 40, 16), (3, 65536, 0, 9), (3, 8192, 64, 16), (4, 8192, 0, 16)])
 def test_gemv_long_rows(owq, bits, K, k, M):
-    shape = (40, K, bits, 128, k, k)
+    shape = (9001 if K == 8192 else 40, K, bits, 128, k, k)
     b, Wg, Wu = block(owq, *shape)
     x = activations(M, M, K)
     want, bound = ref.forward(x, Wg, Wu, "silu")

@@ -54,7 +54,7 @@ struct GatedGemvArgs {
   const __half* x;
   __half* h;
   int N, K, M, act;
-  int tiles;                    // pair tiles, ceil(N / 16)
+  int tile0, tiles;             // this launch's pair tiles, of ceil(N / 16)
   int cl;                       // CTAs of a cluster
   int sub, stages;              // units per ring item, ring stages
   int tcap;                     // most tiles of a cluster
@@ -72,19 +72,18 @@ struct Unit {
 template <int BITS>
 constexpr int stage_bytes(int sub, bool pg) { return sub * 2 * (Unit<BITS>::kTileBlk + (pg ? 64 : 0)); }
 
-// shared memory: ring | barriers (a stage's copies, x) | early segments [tcap][2][16][MT] fp32 | weak
-// sums of the CTA's share of the tiles [wcap][2][16][MT] fp32 | per-channel (scale, zero) pairs
-// [tcap][2][16] | weak indices [2][16 nsl] | activations [M][128 bcap + 8] (later the CTA's sums
-// [tcap][2][16][MT])
+// shared memory: ring | barriers (a stage's copies, x, weak sums) | per tile, the weak columns' sums
+// and the segment that ends the tile, when its warp goes on [tcap][2][16][MT] fp32 | per-channel
+// (scale, zero) pairs [tcap][2][16] | weak indices [2][16 nsl] | activations [M][128 bcap + 8] (later
+// the CTA's sums [tcap][2][16][MT])
 struct SmemPlan {
-  int bars, early, weak, sz, idx, x, total;
+  int bars, early, sz, idx, x, total;
 };
 __host__ __device__ inline SmemPlan smem_plan(const GatedGemvArgs& a, int stage, int MT, bool pg, bool xsmem) {
   SmemPlan p;
   p.bars = kWarps * a.stages * stage;
-  p.early = p.bars + ((kWarps * a.stages + 1) * 8 + 15) / 16 * 16;
-  p.weak = p.early + a.tcap * 32 * MT * 4;
-  p.sz = p.weak + (a.nsl[0] + a.nsl[1] > 0 ? (a.tcap + a.cl - 1) / a.cl * 32 * MT * 4 : 0);
+  p.early = p.bars + ((kWarps * a.stages + 2) * 8 + 15) / 16 * 16;
+  p.sz = p.early + a.tcap * 32 * MT * 4;
   p.idx = p.sz + (pg ? 0 : a.tcap * 32 * 4);
   p.x = p.idx + (a.nsl[0] + a.nsl[1]) * 16 * 4;
   const int rows = xsmem ? a.M * (a.bcap * kBlockCodes + 8) * 2 : 0, sums = a.cl > 1 ? a.tcap * 32 * MT * 4 : 0;
@@ -111,18 +110,18 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + sp.bars) + warp * S;   // this warp's stages
   uint64_t* xbar = reinterpret_cast<uint64_t*>(smem + sp.bars) + kWarps * S;
+  uint64_t* wbar = xbar + 1;
   float* early = reinterpret_cast<float*>(smem + sp.early);
-  float* s_weak = reinterpret_cast<float*>(smem + sp.weak);
   uint32_t* s_sz = reinterpret_cast<uint32_t*>(smem + sp.sz);
   int32_t* s_idx = reinterpret_cast<int32_t*>(smem + sp.idx);   // the gate's, then the up layer's; -1: padding
 
   // this cluster's pair tiles, this CTA's blocks of each, a warp's run of them
   const int rank = CL > 1 ? (int)cluster_ctarank() : 0, cluster = (int)blockIdx.x / CL, clusters = (int)gridDim.x / CL;
-  const int t0 = (int)((long long)cluster * a.tiles / clusters);
-  const int T = (int)((long long)(cluster + 1) * a.tiles / clusters) - t0;
+  const int t0 = a.tile0 + (int)((long long)cluster * a.tiles / clusters);
+  const int T = a.tile0 + (int)((long long)(cluster + 1) * a.tiles / clusters) - t0;
   const int b0 = rank * Kb / CL, nb = (rank + 1) * Kb / CL - b0;
   const int U = nb;                                    // units of a tile in this CTA
-  const int tw0 = rank * T / CL, nwt = (rank + 1) * T / CL - tw0;   // the tiles whose weak columns are this CTA's
+  const bool weak = a.nsl[0] + a.nsl[1] > 0;
   const int share = max(1, (T * U + kWarps - 1) / kWarps);
 
   const int lo = min(warp * share, T * U), hi = min(lo + share, T * U);
@@ -167,7 +166,10 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
 
   if (lane == 0) {
     for (int i = 0; i < S; ++i) mbar_init(&bars[i], 1);
-    if (warp == 0) mbar_init(xbar, 1);
+    if (warp == 0) {
+      mbar_init(xbar, 1);
+      mbar_init(wbar, kWarps);
+    }
     fence_mbar_init();
     point();
     for (int i = 0; i < S; ++i) issue();   // the weights do not depend on the previous kernel
@@ -180,21 +182,42 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
   if constexpr (!PG)
     for (int e = threadIdx.x; e < T * 32; e += kThreads)   // [tile][layer][row]
       s_sz[e] = reinterpret_cast<const uint32_t*>(a.sz_t[(e >> 4) & 1])[(size_t)(t0 + (e >> 5)) * 16 + (e & 15)];
-  // weak items: layer i & 1 of tile tw0 + i / 2 for i = warp, warp + 16, ...; the first four 16-column
-  // slices of the next one are fetched ahead (the weak block is static)
+  // weak items: layer i & 1 of tile i / 2 for i = warp, warp + 16, ...; the first four 16-column
+  // slices of the next one are fetched ahead (the weak block is static).  A CTA takes the weak columns
+  // of its own blocks, a run of slots since the indices ascend.
   uint32_t wf[4][4];
+  int sl_lo[2] = {0, 0}, sl_hi[2] = {a.nsl[0], a.nsl[1]};
   auto weak_frag = [&](int item, int sl, uint32_t (&f)[4]) {
     const int l = item & 1;
-    if (item < 2 * nwt && sl < a.nsl[l]) {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(a.w_weak_t[l]) + ((size_t)(t0 + tw0 + item / 2) * a.nsl[l] + sl) * 128 +
+    if (item < 2 * T && sl < (l ? sl_hi[1] : sl_hi[0])) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(a.w_weak_t[l]) + ((size_t)(t0 + item / 2) * a.nsl[l] + sl) * 128 +
                           (lane >> 2) * 8 + (lane & 3);
       f[0] = __ldg(p); f[1] = __ldg(p + 64); f[2] = __ldg(p + 4); f[3] = __ldg(p + 68);
     }
   };
-  #pragma unroll
-  for (int sl = 0; sl < 4; ++sl) weak_frag(warp, sl, wf[sl]);
+  auto weak_first = [&](int item) {   // the item's first four slices
+    #pragma unroll
+    for (int q = 0; q < 4; ++q) weak_frag(item, ((item & 1) ? sl_lo[1] : sl_lo[0]) + q, wf[q]);
+  };
+  if (weak && CL == 1) weak_first(warp);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();   // barriers, indices, pairs
+  if (weak && CL > 1) {
+    #pragma unroll
+    for (int l = 0; l < 2; ++l) {
+      const int32_t* ix = s_idx + (l ? a.nsl[0] * 16 : 0);
+      int below = 0, upto = 0;   // slots below this CTA's columns, and up to their end
+      for (int t = lane; t < a.k[l]; t += 32) {
+        below += ix[t] < b0 * kBlockCodes;
+        upto += ix[t] < (b0 + nb) * kBlockCodes;
+      }
+      below = __reduce_add_sync(0xffffffffu, below);
+      upto = __reduce_add_sync(0xffffffffu, upto);
+      sl_lo[l] = below / 16;
+      sl_hi[l] = upto > below ? (upto + 15) / 16 : below / 16;
+    }
+    weak_first(warp);
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");   // x and h belong to the previous kernel
   if constexpr (XSMEM) {
     if (threadIdx.x == 0) {
@@ -220,52 +243,55 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
       xg[nt] = a.x + (size_t)min(8 * nt + g, M - 1) * K + b0 * kBlockCodes + 2 * tig;
     }
 
-    for (int item = warp; item < (a.nsl[0] + a.nsl[1] > 0 ? 2 * nwt : 0) && ok; item += kWarps) {
-      const int l = item & 1;
+    for (int item = warp; weak && item < 2 * T && ok; item += kWarps) {
+      const int l = item & 1, s_lo = l ? sl_lo[1] : sl_lo[0], s_hi = l ? sl_hi[1] : sl_hi[0];
       float d[NT][4];
       #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         #pragma unroll
         for (int i = 0; i < 4; ++i) d[nt][i] = 0.f;
       #pragma unroll 1
-      for (int s0 = 0; s0 < a.nsl[l]; s0 += 4) {
-        uint32_t f[4][4];
+      for (int s0 = s_lo; s0 < s_hi; s0 += 4) {
+        uint32_t xw[4][NT][2];   // the activations of slots 16 (s0 + q) + 8 v + 2 tig, + 1 of token 8 nt + g
         #pragma unroll
         for (int q = 0; q < 4; ++q)
           #pragma unroll
-          for (int i = 0; i < 4; ++i) f[q][i] = wf[q][i];
-        const bool more = s0 + 4 < a.nsl[l];
-        #pragma unroll
-        for (int q = 0; q < 4; ++q) weak_frag(more ? item : item + kWarps, more ? s0 + 4 + q : q, wf[q]);
-        #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (s0 + q >= a.nsl[l]) break;
-          #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            uint32_t b[2] = {0u, 0u};   // slots 16 (s0 + q) + 8 v + 2 tig, + 1 of token 8 nt + g
+          for (int v = 0; v < 2; ++v) {
+            const int at = (l ? a.nsl[0] * 16 : 0) + 16 * (s0 + q) + 8 * v + 2 * tig;
+            int2 col = make_int2(-1, -1);
+            if (s0 + q < s_hi) col = *reinterpret_cast<const int2*>(s_idx + at);
+            // (padding and other CTAs' columns: 0; the padded weights are 0 and x may be infinite)
+            const int c0 = col.x - b0 * kBlockCodes, c1 = col.y - b0 * kBlockCodes, nc = nb * kBlockCodes;
+            const bool in0 = col.x >= 0 && c0 >= 0 && c0 < nc && in_range(col.x, K, a.status);
+            const bool in1 = col.y >= 0 && c1 >= 0 && c1 < nc && in_range(col.y, K, a.status);
             #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int col = s_idx[(l ? a.nsl[0] * 16 : 0) + 16 * (s0 + q) + 8 * (e >> 1) + 2 * tig + (e & 1)], tok = min(8 * nt + g, M - 1);
-              if (col >= 0 && in_range(col, K, a.status)) {   // (padding: 0; the padded weights are 0 and x may be infinite)
-                const __half xv = XSMEM && CL == 1 ? xs[(size_t)tok * (a.bcap * kBlockCodes + 8) + col] : a.x[(size_t)tok * K + col];
-                b[e >> 1] |= (uint32_t)__half_as_ushort(xv) << (16 * (e & 1));
-              }
+            for (int nt = 0; nt < NT; ++nt) {
+              const int tok = min(8 * nt + g, M - 1);
+              const __half* row = XSMEM ? xs + (size_t)tok * (a.bcap * kBlockCodes + 8) : a.x + (size_t)tok * K + b0 * kBlockCodes;
+              const uint32_t lo16 = in0 ? __half_as_ushort(row[c0]) : 0, hi16 = in1 ? __half_as_ushort(row[c1]) : 0;
+              xw[q][nt][v] = lo16 | hi16 << 16;
             }
-            mma_16816(d[nt], f[q], b[0], b[1]);
           }
+        #pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (s0 + q < s_hi)
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_16816(d[nt], wf[q], xw[q][nt][0], xw[q][nt][1]);
+        if (s0 + 4 < s_hi) {
+          #pragma unroll
+          for (int q = 0; q < 4; ++q) weak_frag(item, s0 + 4 + q, wf[q]);
         }
       }
-      if (a.nsl[l] == 0) {   // (the next item's fragments all the same)
-        #pragma unroll
-        for (int q = 0; q < 4; ++q) weak_frag(item + kWarps, q, wf[q]);
-      }
-      float* dst = s_weak + (size_t)item * 16 * MT;
+      weak_first(item + kWarps);
+      float* dst = early + (size_t)item * 16 * MT;
       #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         #pragma unroll
         for (int i = 0; i < 2; ++i)
           *reinterpret_cast<float2*>(dst + (g + 8 * i) * MT + 8 * nt + 2 * tig) = make_float2(d[nt][2 * i], d[nt][2 * i + 1]);
     }
+    __syncwarp();
+    if (weak && lane == 0) mbar_arrive(wbar);
 
     float D[2][NT][4];   // [row half][token tile]: rows 8 half + g, (gate, gate, up, up) x tokens
     #pragma unroll
@@ -274,16 +300,18 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
       for (int nt = 0; nt < NT; ++nt)
         #pragma unroll
         for (int i = 0; i < 4; ++i) D[h][nt][i] = 0.f;
-    // a segment's sums: [gate, up][16 rows][MT]
-    auto put = [&](float* dst) {
+    // a segment's sums: [gate, up][16 rows][MT]; `onto` what is there
+    auto put = [&](float* dst, bool onto) {
       #pragma unroll
       for (int h = 0; h < 2; ++h)
         #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
           #pragma unroll
           for (int l = 0; l < 2; ++l) {
-            *reinterpret_cast<float2*>(dst + (l * 16 + 8 * h + g) * MT + 8 * nt + 2 * tig) =
-                make_float2(D[h][nt][2 * l], D[h][nt][2 * l + 1]);
+            float2* p = reinterpret_cast<float2*>(dst + (l * 16 + 8 * h + g) * MT + 8 * nt + 2 * tig);
+            float2 v = make_float2(D[h][nt][2 * l], D[h][nt][2 * l + 1]);
+            if (onto) v = make_float2(p->x + v.x, p->y + v.y);
+            *p = v;
             D[h][nt][2 * l] = 0.f;
             D[h][nt][2 * l + 1] = 0.f;
           }
@@ -366,7 +394,10 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
       u += cnt;
       if (u == U) {
         u = 0;
-        if (left > 0) put(early + (size_t)lt * 32 * MT);   // this run goes on into the next tile
+        if (left > 0) {   // this run goes on into the next tile
+          if (weak) ok = __all_sync(0xffffffffu, mbar_wait(wbar, 0, a.status, a.wait_limit));
+          put(early + (size_t)lt * 32 * MT, weak);
+        }
         ++lt;
       }
     }
@@ -377,23 +408,24 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
         if (++st == S) { st = 0; phase ^= 1u; }
       }
     }
-    if (ok && hi > lo) put(reinterpret_cast<float*>(smem + (size_t)warp * S * stage));   // the run's last segment: its ring is idle
+    if (ok && hi > lo) put(reinterpret_cast<float*>(smem + (size_t)warp * S * stage), false);   // the run's last segment: its ring is idle
   }
   ok = __syncthreads_and(ok);
 
   // the segments of tile t in unit order: this CTA's sums of one (row, token)
   auto segments = [&](int t, int row, int m, float& gs, float& us) {
+    const int f = t * U / share, e = ((t + 1) * U - 1) / share;
+    // the last warp's segment is with the weak sums if its run goes on beyond the tile, else (as the
+    // other warps') in its ring
+    const bool on = min((e + 1) * share, T * U) > (t + 1) * U;
     gs = us = 0.f;
-    if (a.nsl[0] + a.nsl[1] > 0 && t >= tw0 && t < tw0 + nwt) {
-      const float* src = s_weak + (size_t)(t - tw0) * 32 * MT;
+    if (weak || on) {
+      const float* src = early + (size_t)t * 32 * MT;
       gs = src[row * MT + m];
       us = src[(16 + row) * MT + m];
     }
-    const int f = t * U / share, e = ((t + 1) * U - 1) / share;
-    for (int w = f; w <= e; ++w) {
-      // warp w's last segment is on this tile unless its run goes on beyond it
-      const float* src = min((w + 1) * share, T * U) <= (t + 1) * U
-                             ? reinterpret_cast<const float*>(smem + (size_t)w * S * stage) : early + (size_t)t * 32 * MT;
+    for (int w = f; w < e + !on; ++w) {
+      const float* src = reinterpret_cast<const float*>(smem + (size_t)w * S * stage);
       gs += src[row * MT + m];
       us += src[(16 + row) * MT + m];
     }
@@ -442,54 +474,67 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
   cluster_sync();   // no CTA leaves while its sums may still be read
 }
 
-// Items and rings that fit beside the activations, the cheapest first: large items and deep rings;
-// then the same with K split over 2, 4 and 8 CTAs; then the activations from global memory.  (A
-// ring stage in flight per warp covers the latency of the loads from about 40 KB an SM.)
+// Items and rings that fit beside the activations, the largest items first (an item costs a warp
+// about 70 instructions beside the 300 of each unit; one stage in flight per warp covers the
+// latency of the loads from about 40 KB an SM); then the same with K split over 2, 4 and 8 CTAs;
+// then, since a cluster's sums grow with its tiles, the tiles over several launches; then the
+// activations from global memory.
 template <int BITS, int NT, bool PG>
 cudaError_t launch_p(GatedGemvArgs& a, int sms, int dev, cudaStream_t s) {
   static std::atomic<unsigned long long> allowed[2];   // [activations in shared memory]
-  static constexpr int kShapes[][2] = {{4, 3}, {4, 2}, {2, 4}, {2, 3}, {2, 2}, {1, 4}, {1, 3}};
-  static constexpr int kModes[][2] = {{1, 1}, {2, 1}, {4, 1}, {8, 1}, {1, 0}};   // CTAs of a cluster, activations in shared memory
-  void (*kern)(GatedGemvArgs) = nullptr;
-  int smem = 0, in_smem = 0, grid = 0;
-  for (const auto& mode : kModes) {
+  static constexpr int kShapes[][2] = {{4, 2}, {3, 2}, {2, 2}, {1, 3}};
+  const int all = a.tiles;
+  int pieces = 0, smem = 0, xs = 0;
+  auto fits = [&](int cl, int n, int x) {
+    a.cl = cl;
+    a.tiles = (all + n - 1) / n;
+    const int clusters = std::max(1, std::min(a.tiles, sms / cl));
+    a.tcap = (a.tiles + clusters - 1) / clusters;
+    a.bcap = (a.K / kBlockCodes + cl - 1) / cl;
+    if (a.K / kBlockCodes < cl) return false;
     for (const auto& sh : kShapes) {
-        a.cl = mode[0];
-        const int clusters = std::max(1, std::min(a.tiles, sms / a.cl));
-        a.tcap = (a.tiles + clusters - 1) / clusters;
-        a.bcap = (a.K / kBlockCodes + a.cl - 1) / a.cl;
-        a.sub = sh[0];
-        a.stages = sh[1];
-        const int total = smem_plan(a, stage_bytes<BITS>(sh[0], PG), 8 * NT, PG, mode[1]).total;
-        if (total > kMaxSmem || a.K / kBlockCodes < a.cl) continue;
-        smem = total;
-        in_smem = mode[1];
-        grid = clusters * a.cl;
-        kern = in_smem ? k_gated_gemv<BITS, NT, PG, true> : k_gated_gemv<BITS, NT, PG, false>;
-        break;
+      a.sub = sh[0];
+      a.stages = sh[1];
+      smem = smem_plan(a, stage_bytes<BITS>(sh[0], PG), 8 * NT, PG, x).total;
+      if (smem <= kMaxSmem) {
+        pieces = n;
+        xs = x;
+        return true;
       }
-    if (kern) break;
-  }
-  if (!kern) return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem((const void*)kern, kMaxSmem, dev, allowed[in_smem]);
+    }
+    return false;
+  };
+  for (int n = 1; n <= 16 && !pieces; n *= 2)
+    for (int cl = 1; cl <= 8 && !pieces; cl *= 2) fits(cl, n, 1);
+  for (int n = 1; n <= 1024 && !pieces; n *= 2) fits(1, n, 0);
+  if (!pieces) return cudaErrorInvalidValue;
+  auto kern = xs ? k_gated_gemv<BITS, NT, PG, true> : k_gated_gemv<BITS, NT, PG, false>;
+  cudaError_t e = allow_smem((const void*)kern, kMaxSmem, dev, allowed[xs]);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)a.cl;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.cl > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kern, a);
-  if (e != cudaSuccess) allowed[in_smem] = 0;
-  return e;
+  const int per = a.tiles;
+  for (a.tile0 = 0; a.tile0 < all; a.tile0 += per) {
+    a.tiles = std::min(per, all - a.tile0);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(std::max(1, std::min(a.tiles, sms / a.cl)) * a.cl);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.cl;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cl > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kern, a);
+    if (e != cudaSuccess) {
+      allowed[xs] = 0;
+      return e;
+    }
+  }
+  return cudaSuccess;
 }
 
 template <int BITS>
