@@ -54,11 +54,13 @@ struct GatedGemvArgs {
   const __half* x;
   __half* h;
   int N, K, M, act;
-  int tile0, tiles;             // this launch's pair tiles, of ceil(N / 16)
-  int cl;                       // CTAs of a cluster
+  int tile0;                    // this launch's first pair tile, of ceil(N / 16)
+  int base, extra;              // tiles of a cluster: base, and one more in the first `extra`
+  int cl, log_cl;               // CTAs of a cluster (a power of two)
   int sub, stages;              // units per ring item, ring stages
   int tcap;                     // most tiles of a cluster
   int bcap;                     // most 128-column blocks of a CTA
+  int o_bars, o_early, o_sz, o_idx, o_x;   // shared memory offsets
   int* status;
   long long wait_limit;
   uint16_t idx16[2][kParamIdx]; // the first weak indices (a load would cost the prologue its latency)
@@ -76,19 +78,14 @@ constexpr int stage_bytes(int sub, bool pg) { return sub * 2 * (Unit<BITS>::kTil
 // and the segment that ends the tile, when its warp goes on [tcap][2][16][MT] fp32 | per-channel
 // (scale, zero) pairs [tcap][2][16] | weak indices [2][16 nsl] | activations [M][128 bcap + 8] (later
 // the CTA's sums [tcap][2][16][MT])
-struct SmemPlan {
-  int bars, early, sz, idx, x, total;
-};
-__host__ __device__ inline SmemPlan smem_plan(const GatedGemvArgs& a, int stage, int MT, bool pg, bool xsmem) {
-  SmemPlan p;
-  p.bars = kWarps * a.stages * stage;
-  p.early = p.bars + ((kWarps * a.stages + 2) * 8 + 15) / 16 * 16;
-  p.sz = p.early + a.tcap * 32 * MT * 4;
-  p.idx = p.sz + (pg ? 0 : a.tcap * 32 * 4);
-  p.x = p.idx + (a.nsl[0] + a.nsl[1]) * 16 * 4;
+inline int smem_plan(GatedGemvArgs& a, int stage, int MT, bool pg, bool xsmem) {   // its size
+  a.o_bars = kWarps * a.stages * stage;
+  a.o_early = a.o_bars + ((kWarps * a.stages + 2) * 8 + 15) / 16 * 16;
+  a.o_sz = a.o_early + a.tcap * 32 * MT * 4;
+  a.o_idx = a.o_sz + (pg ? 0 : a.tcap * 32 * 4);
+  a.o_x = a.o_idx + (a.nsl[0] + a.nsl[1]) * 16 * 4;
   const int rows = xsmem ? a.M * (a.bcap * kBlockCodes + 8) * 2 : 0, sums = a.cl > 1 ? a.tcap * 32 * MT * 4 : 0;
-  p.total = p.x + (rows > sums ? rows : sums);
-  return p;
+  return a.o_x + std::max(rows, sums);
 }
 
 __device__ __forceinline__ uint32_t lds_u1(uint32_t a) {
@@ -106,23 +103,22 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
   const int K = a.K, Kb = K / kBlockCodes, M = a.M, S = a.stages, sub = a.sub, CL = a.cl;
   const int stage = stage_bytes<BITS>(sub, PG);
-  const SmemPlan sp = smem_plan(a, stage, MT, PG, XSMEM);
   const uint32_t sbase = smem_u32(smem);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + sp.bars) + warp * S;   // this warp's stages
-  uint64_t* xbar = reinterpret_cast<uint64_t*>(smem + sp.bars) + kWarps * S;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + a.o_bars) + warp * S;   // this warp's stages
+  uint64_t* xbar = reinterpret_cast<uint64_t*>(smem + a.o_bars) + kWarps * S;
   uint64_t* wbar = xbar + 1;
-  float* early = reinterpret_cast<float*>(smem + sp.early);
-  uint32_t* s_sz = reinterpret_cast<uint32_t*>(smem + sp.sz);
-  int32_t* s_idx = reinterpret_cast<int32_t*>(smem + sp.idx);   // the gate's, then the up layer's; -1: padding
+  float* early = reinterpret_cast<float*>(smem + a.o_early);
+  uint32_t* s_sz = reinterpret_cast<uint32_t*>(smem + a.o_sz);
+  int32_t* s_idx = reinterpret_cast<int32_t*>(smem + a.o_idx);   // the gate's, then the up layer's; -1: padding
 
   // this cluster's pair tiles, this CTA's blocks of each, a warp's run of them
-  const int rank = CL > 1 ? (int)cluster_ctarank() : 0, cluster = (int)blockIdx.x / CL, clusters = (int)gridDim.x / CL;
-  const int t0 = a.tile0 + (int)((long long)cluster * a.tiles / clusters);
-  const int T = a.tile0 + (int)((long long)(cluster + 1) * a.tiles / clusters) - t0;
-  const int b0 = rank * Kb / CL, nb = (rank + 1) * Kb / CL - b0;
+  // (no division before the first copies: the prologue is not hidden behind anything)
+  const int rank = CL > 1 ? (int)cluster_ctarank() : 0, cluster = (int)blockIdx.x >> a.log_cl;
+  const int t0 = a.tile0 + cluster * a.base + min(cluster, a.extra), T = a.base + (cluster < a.extra);
+  const int b0 = (rank * Kb) >> a.log_cl, nb = (((rank + 1) * Kb) >> a.log_cl) - b0;
   const int U = nb;                                    // units of a tile in this CTA
   const bool weak = a.nsl[0] + a.nsl[1] > 0;
-  const int share = max(1, (T * U + kWarps - 1) / kWarps);
+  const int share = (T * U + kWarps - 1) / kWarps;   // (T and U are at least 1)
 
   const int lo = min(warp * share, T * U), hi = min(lo + share, T * U);
 
@@ -224,7 +220,7 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
       const uint32_t bytes = (uint32_t)(nb * kBlockCodes * 2);
       mbar_arrive_expect_tx(xbar, (uint32_t)M * bytes);
       for (int m = 0; m < M; ++m)
-        bulk_load(smem + sp.x + (size_t)m * (a.bcap * kBlockCodes + 8) * 2, a.x + (size_t)m * K + b0 * kBlockCodes, bytes, xbar);
+        bulk_load(smem + a.o_x + (size_t)m * (a.bcap * kBlockCodes + 8) * 2, a.x + (size_t)m * K + b0 * kBlockCodes, bytes, xbar);
     }
   }
   bool ok = true;    // uniform per warp
@@ -236,10 +232,10 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
     // columns each); tokens past M repeat the last one (their sums are not stored)
     uint32_t xa[NT];
     const __half* xg[NT];
-    const __half* xs = reinterpret_cast<const __half*>(smem + sp.x);
+    const __half* xs = reinterpret_cast<const __half*>(smem + a.o_x);
     #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      xa[nt] = sbase + sp.x + (min(8 * nt + (lane & 7), M - 1) * (a.bcap * kBlockCodes + 8) + 8 * (lane >> 3)) * 2;
+      xa[nt] = sbase + a.o_x + (min(8 * nt + (lane & 7), M - 1) * (a.bcap * kBlockCodes + 8) + 8 * (lane >> 3)) * 2;
       xg[nt] = a.x + (size_t)min(8 * nt + g, M - 1) * K + b0 * kBlockCodes + 2 * tig;
     }
 
@@ -257,9 +253,8 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
         for (int q = 0; q < 4; ++q)
           #pragma unroll
           for (int v = 0; v < 2; ++v) {
-            const int at = (l ? a.nsl[0] * 16 : 0) + 16 * (s0 + q) + 8 * v + 2 * tig;
-            int2 col = make_int2(-1, -1);
-            if (s0 + q < s_hi) col = *reinterpret_cast<const int2*>(s_idx + at);
+            if (s0 + q >= s_hi) continue;
+            const int2 col = *reinterpret_cast<const int2*>(s_idx + (l ? a.nsl[0] * 16 : 0) + 16 * (s0 + q) + 8 * v + 2 * tig);
             // (padding and other CTAs' columns: 0; the padded weights are 0 and x may be infinite)
             const int c0 = col.x - b0 * kBlockCodes, c1 = col.y - b0 * kBlockCodes, nc = nb * kBlockCodes;
             const bool in0 = col.x >= 0 && c0 >= 0 && c0 < nc && in_range(col.x, K, a.status);
@@ -451,7 +446,7 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
   }
   // several CTAs: each leaves its sums where its activations were, then finishes its share of the
   // outputs from everybody's, in rank order
-  float* sums = reinterpret_cast<float*>(smem + sp.x);   // [output][gate, up]
+  float* sums = reinterpret_cast<float*>(smem + a.o_x);   // [output][gate, up]
   for (int e = threadIdx.x; e < outs; e += kThreads) {
     const int row = e & 15, tm = e >> 4, t = tm / M, m = tm - t * M;
     float gs, us;
@@ -480,22 +475,21 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
 // then, since a cluster's sums grow with its tiles, the tiles over several launches; then the
 // activations from global memory.
 template <int BITS, int NT, bool PG>
-cudaError_t launch_p(GatedGemvArgs& a, int sms, int dev, cudaStream_t s) {
+cudaError_t launch_p(GatedGemvArgs& a, int all, int sms, int dev, cudaStream_t s) {
   static std::atomic<unsigned long long> allowed[2];   // [activations in shared memory]
   static constexpr int kShapes[][2] = {{4, 2}, {3, 2}, {2, 2}, {1, 3}};
-  const int all = a.tiles;
-  int pieces = 0, smem = 0, xs = 0;
+  int pieces = 0, smem = 0, xs = 0, per = 0;
   auto fits = [&](int cl, int n, int x) {
     a.cl = cl;
-    a.tiles = (all + n - 1) / n;
-    const int clusters = std::max(1, std::min(a.tiles, sms / cl));
-    a.tcap = (a.tiles + clusters - 1) / clusters;
+    per = (all + n - 1) / n;
+    const int clusters = std::max(1, std::min(per, sms / cl));
+    a.tcap = (per + clusters - 1) / clusters;
     a.bcap = (a.K / kBlockCodes + cl - 1) / cl;
     if (a.K / kBlockCodes < cl) return false;
     for (const auto& sh : kShapes) {
       a.sub = sh[0];
       a.stages = sh[1];
-      smem = smem_plan(a, stage_bytes<BITS>(sh[0], PG), 8 * NT, PG, x).total;
+      smem = smem_plan(a, stage_bytes<BITS>(sh[0], PG), 8 * NT, PG, x);
       if (smem <= kMaxSmem) {
         pieces = n;
         xs = x;
@@ -511,11 +505,13 @@ cudaError_t launch_p(GatedGemvArgs& a, int sms, int dev, cudaStream_t s) {
   auto kern = xs ? k_gated_gemv<BITS, NT, PG, true> : k_gated_gemv<BITS, NT, PG, false>;
   cudaError_t e = allow_smem((const void*)kern, kMaxSmem, dev, allowed[xs]);
   if (e != cudaSuccess) return e;
-  const int per = a.tiles;
+  for (a.log_cl = 0; 1 << a.log_cl < a.cl;) ++a.log_cl;
   for (a.tile0 = 0; a.tile0 < all; a.tile0 += per) {
-    a.tiles = std::min(per, all - a.tile0);
+    const int tiles = std::min(per, all - a.tile0), clusters = std::max(1, std::min(tiles, sms / a.cl));
+    a.base = tiles / clusters;
+    a.extra = tiles % clusters;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(std::max(1, std::min(a.tiles, sms / a.cl)) * a.cl);
+    cfg.gridDim = dim3(clusters * a.cl);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -538,9 +534,9 @@ cudaError_t launch_p(GatedGemvArgs& a, int sms, int dev, cudaStream_t s) {
 }
 
 template <int BITS>
-cudaError_t launch_b(GatedGemvArgs& a, bool pg, int sms, int dev, cudaStream_t s) {
-  if (a.M <= 8) return pg ? launch_p<BITS, 1, true>(a, sms, dev, s) : launch_p<BITS, 1, false>(a, sms, dev, s);
-  return pg ? launch_p<BITS, 2, true>(a, sms, dev, s) : launch_p<BITS, 2, false>(a, sms, dev, s);
+cudaError_t launch_b(GatedGemvArgs& a, bool pg, int all, int sms, int dev, cudaStream_t s) {
+  if (a.M <= 8) return pg ? launch_p<BITS, 1, true>(a, all, sms, dev, s) : launch_p<BITS, 1, false>(a, all, sms, dev, s);
+  return pg ? launch_p<BITS, 2, true>(a, all, sms, dev, s) : launch_p<BITS, 2, false>(a, all, sms, dev, s);
 }
 
 }  // namespace
@@ -565,11 +561,11 @@ cudaError_t launch_gated_gemv(const Layer& gate, const Layer& up, int act, const
   a.K = gate.K;
   a.M = M;
   a.act = act;
-  a.tiles = (gate.N + 15) / 16;
+  const int all = (gate.N + 15) / 16;   // pair tiles
   a.status = gate.status;
   a.wait_limit = wait_limit;
   const int sms = layer_sm_count(gate.device);
-  return gate.bits == 3 ? launch_b<3>(a, gate.G > 1, sms, gate.device, s) : launch_b<4>(a, gate.G > 1, sms, gate.device, s);
+  return gate.bits == 3 ? launch_b<3>(a, gate.G > 1, all, sms, gate.device, s) : launch_b<4>(a, gate.G > 1, all, sms, gate.device, s);
 }
 
 }  // namespace owq
