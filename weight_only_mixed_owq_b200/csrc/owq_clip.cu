@@ -6,29 +6,34 @@
 // before the first can be written, so what does not stay on the chip is read again.
 //
 // One cooperative launch of one CTA per SM.  The tensors are cut into chunks dealt round-robin to
-// the CTAs; each CTA keeps its first chunks in shared memory (about 190 KB per SM), streams the
-// others, adds the squares in fp64 (no overflow, underflow or cancellation at any length; the
-// conversions stay far below the memory time), publishes its partial sum and waits for the
-// others' (bounded).  The second pass walks the chunks backwards: the last ones read are still in
-// L2, and the streaming stores leave them there until they are read.  All sums run in a fixed
-// order: repeated calls give identical bits.
+// the CTAs.  A producer warp streams a CTA's chunks through a ring of bulk copies (up to 192 KB in
+// flight, no registers behind it); 16 warps add the squares; the CTA publishes its partial sum and
+// waits for the others' (bounded).  The second pass walks the chunks backwards: the last ones are
+// still in the ring, the ones before them in L2, where the streaming stores leave them until they
+// are read.
+// Squares are added in fp64, eight values' worth at a time: those are summed in fp32 (2^-24 each,
+// averaging out) where that neither overflows nor loses small values, else one by one in fp64 (a
+// conversion per value would take as long as the memory).  All sums run in a fixed order: repeated
+// calls give identical bits.
 #include <cuda_bf16.h>
 
 #include "owq_internal.cuh"
+#include "owq_sm100.cuh"
 
 namespace owq {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kSlotBytes = 64 * 1024;   // most bytes of a chunk
-constexpr int kCacheBytes = 3 * kSlotBytes;
+using namespace sm100;
+
+constexpr int kWarps = 16, kThreads = kWarps * 32;   // and the producer warp
+constexpr int kChunkBytes = 32 * 1024;               // most bytes of a chunk
+constexpr int kRingBytes = 6 * kChunkBytes, kMaxSlots = 16;
 
 struct ClipArgs {
   const ClipChunk* chunks;
   int n_chunks;
-  int slot_bytes;     // bytes a chunk's 16-byte pieces take in shared memory
-  int cached;         // chunks of a CTA kept in shared memory
-  double* part;       // [gridDim.x] partial sums
+  int slot_bytes, slots;
+  double* part;                  // [gridDim.x] partial sums
   unsigned long long* arrived;   // CTAs that have published, over all calls
   float max_norm;
   float* norm;
@@ -68,103 +73,173 @@ struct Cut {
 };
 
 template <int DT>
-__device__ __forceinline__ double squares(const ClipChunk& c, uint4* keep) {
+__device__ __forceinline__ double squares(const ClipChunk& c, const uint4* slot) {
   using T = typename Vec<DT>::T;
   constexpr int P = 16 / sizeof(T);
   const T* in = static_cast<const T*>(c.in);
   const Cut<T> cut(in, c.n);
-  const uint4* v = reinterpret_cast<const uint4*>(in + cut.head);
   double s = 0.0;
   #pragma unroll 4
   for (int i = threadIdx.x; i < cut.pieces; i += kThreads) {
-    const uint4 q = __ldcg(v + i);
-    if (keep) keep[i] = q;
+    const uint4 q = slot[i];
     const T* e = reinterpret_cast<const T*>(&q);
-    if constexpr (DT == OWQ_F16) {   // squares of fp16 values are exact in fp32, and never overflow
-      #pragma unroll
-      for (int j = 0; j < P; j += 2) {
-        const float a = Vec<DT>::get(e[j]), b = Vec<DT>::get(e[j + 1]);
-        s += (double)fmaf(a, a, b * b);
-      }
+    float p = 0.f;
+    #pragma unroll
+    for (int u = 0; u < P; ++u) {
+      const float v = Vec<DT>::get(e[u]);
+      p = fmaf(v, v, p);
+    }
+    if (p >= 1e-25f && p <= 1e37f) {   // (a square lost below 1e-45 is below 2^-66 of the sum)
+      s += (double)p;
     } else {
       #pragma unroll
-      for (int j = 0; j < P; ++j) {
-        const double a = (double)Vec<DT>::get(e[j]);
-        s = fma(a, a, s);
+      for (int u = 0; u < P; ++u) {
+        const double v = (double)Vec<DT>::get(e[u]);
+        s = fma(v, v, s);
       }
     }
   }
   const int tail = cut.head + cut.pieces * P;   // fewer than P values at either end
-  const int i = threadIdx.x < cut.head ? (int)threadIdx.x : tail + (int)threadIdx.x - cut.head;
-  if (i < c.n && (threadIdx.x < cut.head || i >= tail) && threadIdx.x < 2 * P) {
-    const double a = (double)Vec<DT>::get(in[i]);
-    s = fma(a, a, s);
+  const int i = (int)threadIdx.x < cut.head ? (int)threadIdx.x : tail + (int)threadIdx.x - cut.head;
+  if (i < c.n && ((int)threadIdx.x < cut.head || i >= tail) && threadIdx.x < 2 * P) {
+    const double v = (double)Vec<DT>::get(in[i]);
+    s = fma(v, v, s);
   }
   return s;
 }
 
 template <int DT>
-__device__ __forceinline__ void scale(const ClipChunk& c, const uint4* kept, float f) {
+__device__ __forceinline__ void scale(const ClipChunk& c, const uint4* slot, float f) {
   using T = typename Vec<DT>::T;
   constexpr int P = 16 / sizeof(T);
   const T* in = static_cast<const T*>(c.in);
   T* out = static_cast<T*>(c.out);
   const Cut<T> cut(in, c.n);
-  const uint4* v = reinterpret_cast<const uint4*>(in + cut.head);
   T* o = out + cut.head;
   const bool vec = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
   const bool copy = f == 1.f;   // bit for bit (a product would quieten a NaN's payload)
   #pragma unroll 4
   for (int i = threadIdx.x; i < cut.pieces; i += kThreads) {
-    const uint4 q = kept ? kept[i] : __ldcg(v + i);
+    const uint4 q = slot[i];
     const T* e = reinterpret_cast<const T*>(&q);
     uint4 r;
     T* d = reinterpret_cast<T*>(&r);
     #pragma unroll
-    for (int j = 0; j < P; ++j) d[j] = copy ? e[j] : Vec<DT>::put(Vec<DT>::get(e[j]) * f);
+    for (int u = 0; u < P; ++u) d[u] = copy ? e[u] : Vec<DT>::put(Vec<DT>::get(e[u]) * f);
     if (vec) {
       __stcs(reinterpret_cast<uint4*>(o) + i, r);
     } else {
       #pragma unroll
-      for (int j = 0; j < P; ++j) o[(size_t)i * P + j] = d[j];
+      for (int u = 0; u < P; ++u) o[(size_t)i * P + u] = d[u];
     }
   }
   const int tail = cut.head + cut.pieces * P;
-  const int i = threadIdx.x < cut.head ? (int)threadIdx.x : tail + (int)threadIdx.x - cut.head;
-  if (i < c.n && (threadIdx.x < cut.head || i >= tail) && threadIdx.x < 2 * P) out[i] = copy ? in[i] : Vec<DT>::put(Vec<DT>::get(in[i]) * f);
+  const int i = (int)threadIdx.x < cut.head ? (int)threadIdx.x : tail + (int)threadIdx.x - cut.head;
+  if (i < c.n && ((int)threadIdx.x < cut.head || i >= tail) && threadIdx.x < 2 * P)
+    out[i] = copy ? in[i] : Vec<DT>::put(Vec<DT>::get(in[i]) * f);
 }
 
-// sum over the CTA in a fixed order; the result in every thread
+// sum over the consumer warps in a fixed order; the result in every one of their threads
 __device__ __forceinline__ double block_sum(double v, double* s_red) {
   #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = s_red[threadIdx.x & 31];
+  named_bar_sync(1, kThreads);
+  v = s_red[threadIdx.x & (kWarps - 1)];
   #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
+  for (int o = kWarps / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  named_bar_sync(1, kThreads);
   return v;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) k_clip(const __grid_constant__ ClipArgs a) {
-  extern __shared__ __align__(16) unsigned char cache[];
-  __shared__ double s_red[32];
-  __shared__ int s_ok;
-  const int G = gridDim.x, b = blockIdx.x;
-  const int mine = b < a.n_chunks ? (a.n_chunks - 1 - b) / G + 1 : 0;   // chunks b, b + G, ...
+// A CTA's chunk i sits in ring slot i % slots, in the second pass too: the slot of the last chunk of
+// residue s (index last) is used last / slots + 1 times in the first pass and then once for each
+// chunk last - slots, last - 2 slots, ...  `use` is the number of a use, for the barriers' phases.
+struct Uses {
+  int mine, slots;
+  __device__ __forceinline__ int last(int i) const { return i + (mine - 1 - i) / slots * slots; }
+  __device__ __forceinline__ int second(int i) const { return last(i) / slots + (last(i) - i) / slots; }   // (of a copy; last(i): the first pass's)
+};
 
-  double s = 0.0;
-  ClipChunk next = {};
-  if (mine > 0) next = a.chunks[b];
-  for (int i = 0; i < mine; ++i) {
-    const ClipChunk c = next;
-    if (i + 1 < mine) next = a.chunks[b + (size_t)(i + 1) * G];
-    uint4* keep = i < a.cached ? reinterpret_cast<uint4*>(cache + (size_t)i * a.slot_bytes) : nullptr;
-    if (c.dtype == OWQ_F32) s += squares<OWQ_F32>(c, keep);
-    else if (c.dtype == OWQ_F16) s += squares<OWQ_F16>(c, keep);
-    else s += squares<OWQ_BF16>(c, keep);
+__global__ void __launch_bounds__(kThreads + 32, 1) k_clip(const __grid_constant__ ClipArgs a) {
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ ClipChunk s_chunk[kMaxSlots];
+  __shared__ uint64_t full[kMaxSlots], empty[kMaxSlots];
+  __shared__ double s_red[kWarps];
+  __shared__ int s_ok;
+  const int G = gridDim.x, b = blockIdx.x, S = a.slots, lane = threadIdx.x & 31;
+  const int mine = b < a.n_chunks ? (a.n_chunks - 1 - b) / G + 1 : 0;   // chunks b, b + G, ...
+  const Uses uses{mine, S};
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWarps);
+    }
+    fence_mbar_init();
   }
+  __syncthreads();
+
+  if (threadIdx.x >= kThreads) {
+    // ---------------- producer ----------------
+    // one lane copies; the warp fetches the table entries 32 at a time
+    bool ok = true;
+    ClipChunk mineq = {};
+    auto load = [&](int i, const ClipChunk& c) {
+      const int s = i % S, size = c.dtype == OWQ_F32 ? 4 : 2;
+      const int head = min(c.n, (int)((16 - (reinterpret_cast<uintptr_t>(c.in) & 15)) & 15) / size);
+      const uint32_t bytes = (uint32_t)((c.n - head) * size) & ~15u;
+      s_chunk[s] = c;
+      mbar_arrive_expect_tx(&full[s], bytes);
+      if (bytes) bulk_load(ring + (size_t)s * a.slot_bytes, static_cast<const char*>(c.in) + head * size, bytes, &full[s]);
+    };
+    auto entry = [&](int at) {   // of the 32 this warp holds
+      ClipChunk c;
+      c.in = reinterpret_cast<const void*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mineq.in), at));
+      c.out = reinterpret_cast<void*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mineq.out), at));
+      c.n = __shfl_sync(0xffffffffu, mineq.n, at);
+      c.dtype = __shfl_sync(0xffffffffu, mineq.dtype, at);
+      return c;
+    };
+    for (int i = 0; i < mine && ok; ++i) {
+      if (i % 32 == 0 && i + lane < mine) mineq = a.chunks[b + (size_t)(i + lane) * G];
+      const ClipChunk c = entry(i % 32);
+      if (i >= S) ok = __all_sync(0xffffffffu, mbar_wait(&empty[i % S], (uint32_t)(i / S - 1) & 1, a.status, a.wait_limit));
+      if (ok && lane == 0) load(i, c);
+      __syncwarp();
+    }
+    // Every slot's first-pass uses are consumed before the second pass waits on the slots' barriers: a
+    // wait by parity must not be more than one phase ahead of its barrier.
+    named_bar_sync(2, kThreads + 32);
+    for (int k = 0, i = mine - S - 1; i >= 0 && ok; --i, ++k) {   // the second pass, after the resident chunks
+      if (k % 32 == 0 && i - lane >= 0) mineq = a.chunks[b + (size_t)(i - lane) * G];
+      const ClipChunk c = entry(k % 32);
+      // the second pass's use of the slot by chunk i + S is over: its consumption follows the first pass's
+      ok = __all_sync(0xffffffffu, mbar_wait(&empty[i % S], (uint32_t)uses.second(i) & 1, a.status, a.wait_limit));
+      if (ok && lane == 0) load(i, c);
+      __syncwarp();
+    }
+    // never leave with copies in flight: the last copy into every slot
+    if (lane < min(S, mine)) mbar_wait(&full[lane], (uint32_t)(mine > S ? uses.second(lane) : 0) & 1, a.status, a.wait_limit);
+    return;
+  }
+
+  // ---------------- consumers ----------------
+  bool ok = true;   // uniform per warp
+  double s = 0.0;
+  for (int i = 0; i < mine && ok; ++i) {
+    const int sl = i % S;
+    ok = __all_sync(0xffffffffu, mbar_wait(&full[sl], (uint32_t)(i / S) & 1, a.status, a.wait_limit));
+    const uint4* slot = reinterpret_cast<const uint4*>(ring + (size_t)sl * a.slot_bytes);
+    const ClipChunk c = s_chunk[sl];
+    if (ok) {
+      if (c.dtype == OWQ_F32) s += squares<OWQ_F32>(c, slot);
+      else if (c.dtype == OWQ_F16) s += squares<OWQ_F16>(c, slot);
+      else s += squares<OWQ_BF16>(c, slot);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[sl]);
+  }
+  named_bar_sync(2, kThreads + 32);   // the producer's second pass may start
   s = block_sum(s, s_red);
 
   // publish, then wait until every CTA of this call has: the counter only grows, by G a call
@@ -173,45 +248,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_clip(const __grid_constant__ Cl
     __threadfence();
     const unsigned long long old = atomicAdd(a.arrived, 1ull);
     const unsigned long long want = (old / G + 1) * G;
-    int ok = 1;
+    int all = 1;
     const long long t0 = clock64();
     while (*reinterpret_cast<volatile unsigned long long*>(a.arrived) < want)
       if (clock64() - t0 > a.wait_limit) {
         atomicOr(a.status, kStatusTimeout);
-        ok = 0;
+        all = 0;
         break;
       }
     __threadfence();
-    s_ok = ok;
+    s_ok = all;
   }
-  __syncthreads();
-  if (!s_ok) return;
+  named_bar_sync(1, kThreads);
+  ok = ok && s_ok;
   double t = 0.0;
   for (int i = threadIdx.x; i < G; i += kThreads) t += __ldcg(a.part + i);
   t = block_sum(t, s_red);
   const float norm = (float)sqrt(t);
   const float f = norm <= 3.402823466e38f ? fminf(a.max_norm / (norm + 1e-6f), 1.f) : 1.f;   // (false for NaN too)
-  if (b == 0 && threadIdx.x == 0) *a.norm = norm;
+  if (b == 0 && threadIdx.x == 0 && ok) *a.norm = norm;
 
-  if (mine > 0) next = a.chunks[b + (size_t)(mine - 1) * G];
   for (int i = mine - 1; i >= 0; --i) {
-    const ClipChunk c = next;
-    if (i > 0) next = a.chunks[b + (size_t)(i - 1) * G];
-    if (f == 1.f && c.in == c.out) continue;   // in place and unclipped
-    const uint4* kept = i < a.cached ? reinterpret_cast<const uint4*>(cache + (size_t)i * a.slot_bytes) : nullptr;
-    if (c.dtype == OWQ_F32) scale<OWQ_F32>(c, kept, f);
-    else if (c.dtype == OWQ_F16) scale<OWQ_F16>(c, kept, f);
-    else scale<OWQ_BF16>(c, kept, f);
+    const int sl = i % S;
+    if (i < mine - S && ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[sl], (uint32_t)uses.second(i) & 1, a.status, a.wait_limit));
+    const uint4* slot = reinterpret_cast<const uint4*>(ring + (size_t)sl * a.slot_bytes);
+    const ClipChunk c = s_chunk[sl];
+    if (ok && !(f == 1.f && c.in == c.out)) {   // (in place and unclipped: nothing to write)
+      if (c.dtype == OWQ_F32) scale<OWQ_F32>(c, slot, f);
+      else if (c.dtype == OWQ_F16) scale<OWQ_F16>(c, slot, f);
+      else scale<OWQ_BF16>(c, slot, f);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[sl]);
   }
 }
 
 }  // namespace
 
-// Bytes of a chunk: the work of every CTA in about four chunks, so that the deal is even, within
-// 4 KB (a few 16-byte pieces per thread or less: latency) and 64 KB (four pieces in flight each).
+// Bytes of a chunk: the work of every CTA in about eight chunks, so that the deal is even and the
+// ring has something to overlap, within 4 KB (the smallest: latency) and 32 KB.
 int clip_chunk_bytes(long long total_bytes, int sms) {
-  const long long want = total_bytes / (4LL * sms);
-  return (int)std::max<long long>(4096, std::min<long long>(kSlotBytes, (want + 4095) / 4096 * 4096));
+  const long long want = total_bytes / (8LL * sms);
+  return (int)std::max<long long>(4096, std::min<long long>(kChunkBytes, (want + 4095) / 4096 * 4096));
 }
 
 cudaError_t launch_clip(const Clip& c, float max_norm, float* norm, long long wait_limit, cudaStream_t s) {
@@ -226,14 +304,14 @@ cudaError_t launch_clip(const Clip& c, float max_norm, float* norm, long long wa
   a.status = c.status;
   a.wait_limit = wait_limit;
   const int per = (c.n_chunks + c.grid - 1) / c.grid;
-  a.cached = std::min(per, kCacheBytes / c.chunk_bytes);
-  const int smem = a.cached * c.chunk_bytes;
+  a.slots = std::max(1, std::min({per, kRingBytes / c.chunk_bytes, kMaxSlots}));
+  const int smem = a.slots * c.chunk_bytes;
   static std::atomic<unsigned long long> allowed{0};
-  cudaError_t e = allow_smem((const void*)k_clip, kCacheBytes, c.device, allowed);
+  cudaError_t e = allow_smem((const void*)k_clip, kRingBytes, c.device, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(c.grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreads + 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
