@@ -409,10 +409,20 @@ __global__ void k_gated_reduce(const __grid_constant__ GatedGemmParams p, int BN
     const int row = ((tile % p.rts) * 2 + rank) * kHalfRows + r, t = (tile / p.rts) * BN + t0;
     if (row >= p.N || t >= p.M) continue;
     const float* w = p.ws + partial_at(p.split, 0, tile, rank, BN) + (size_t)t0 * kBM + 32 * (r / 16) + r % 16;
-    float gs = w[0], us = w[16];
-    for (int z = 1; z < p.split.splits; ++z) {
-      gs += w[z * stride];
-      us += w[z * stride + 16];
+    float gs = 0.f, us = 0.f;
+    for (int z0 = 0; z0 < p.split.splits; z0 += 8) {   // eight splits' loads in flight
+      float gz[8], uz[8];
+      #pragma unroll
+      for (int z = 0; z < 8; ++z) {
+        const bool ok = z0 + z < p.split.splits;
+        gz[z] = ok ? w[(z0 + z) * stride] : 0.f;
+        uz[z] = ok ? w[(z0 + z) * stride + 16] : 0.f;
+      }
+      #pragma unroll
+      for (int z = 0; z < 8; ++z) {
+        gs += gz[z];
+        us += uz[z];
+      }
     }
     const size_t o = (size_t)t * p.N + row;
     with_act(p.act, [&](auto act) {
@@ -731,10 +741,15 @@ __global__ void k_gated_ig_reduce(const __grid_constant__ GatedIgParams p, int B
     const int c = (int)(e % kBM), t0 = (int)(e / kBM % BN), u = (int)(e / kBM / BN), tile = p.split.whole + u / 2;
     const int b = (tile % Kp) * 2 + u % 2, t = (tile / Kp) * BN + t0;
     if (t >= p.M || b >= Kb) continue;
-    float4 v = *reinterpret_cast<const float4*>(p.ws + e);
-    for (int z = 1; z < p.split.splits; ++z) {
-      const float4 w = *reinterpret_cast<const float4*>(p.ws + (size_t)z * n + e);
-      v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int z0 = 0; z0 < p.split.splits; z0 += 8) {   // eight splits' loads in flight
+      float4 w[8];
+      #pragma unroll
+      for (int z = 0; z < 8; ++z)
+        w[z] = z0 + z < p.split.splits ? *reinterpret_cast<const float4*>(p.ws + (size_t)(z0 + z) * n + e)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+      #pragma unroll
+      for (int z = 0; z < 8; ++z) { v.x += w[z].x; v.y += w[z].y; v.z += w[z].z; v.w += w[z].w; }
     }
     __half2* o = reinterpret_cast<__half2*>(dx + (size_t)t * p.K + b * kStepCodes + c);
     o[0] = __floats2half2_rn(v.x, v.y);
