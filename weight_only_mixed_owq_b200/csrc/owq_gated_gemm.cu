@@ -668,8 +668,13 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
           float v = 0.f;
           if (m0 + tk < p.M) {
             const float* wk = p.wk[l] + (size_t)(first + c) * p.M + m0 + tk;
-            #pragma unroll 8
-            for (int z = 0; z < p.wsplits; ++z) v += __ldcg(wk + z * plane);
+            for (int z0 = 0; z0 < p.wsplits; z0 += 8) {   // eight splits' loads in flight
+              float w[8];
+              #pragma unroll
+              for (int z = 0; z < 8; ++z) w[z] = z0 + z < p.wsplits ? __ldcg(wk + (z0 + z) * plane) : 0.f;
+              #pragma unroll
+              for (int z = 0; z < 8; ++z) v += w[z];
+            }
           }
           s_wk[(n_weak + c) * BN + tk] = v;
         }
@@ -759,9 +764,9 @@ __global__ void k_gated_ig_reduce(const __grid_constant__ GatedIgParams p, int B
 
 // The weak columns' products of both layers, wk[l][row split][slot][m] = sum_i dy_l[m][i]
 // w_weak_l[i][slot] (mma.sync m16n8k16: rows = tokens, K = weight rows, columns = slots).  A CTA of
-// 4 warps computes 64 tokens x CT slots of one layer over one split of the rows, 32 rows at a time
+// 4 warps computes 64 tokens x CT slots of one layer over one split of the rows, 64 rows at a time
 // through a 4-stage cp.async ring.  Bound by reading the gradients, once per CT slots.
-constexpr int kIwTok = 64, kIwRows = 32, kIwThreads = 128, kIwStages = 4, kIwMaxSplits = 8;
+constexpr int kIwTok = 64, kIwRows = 64, kIwThreads = 128, kIwStages = 4, kIwMaxSplits = 16;
 constexpr int kIwDyLd = kIwRows + 8;   // padded row stride (halves)
 
 struct GatedIgwArgs {
@@ -769,12 +774,15 @@ struct GatedIgwArgs {
   const __half* w[2];   // [N][k_ld]
   float* wk[2];
   int k[2], k_ld[2], ctiles0;   // slot tiles of the gate layer (blockIdx.y below it)
-  int N, ldy, M, per;           // per: rows per split, a multiple of 32
+  int N, ldy, M, per;           // per: rows per split, a multiple of kIwRows
 };
 template <int CT>
+constexpr int igw_smem_bytes() { return kIwStages * (kIwTok * kIwDyLd + kIwRows * (CT + 8)) * (int)sizeof(__half); }
+template <int CT>
 __global__ void __launch_bounds__(kIwThreads) k_gated_igw(const __grid_constant__ GatedIgwArgs a) {
-  __shared__ __align__(128) __half s_dy[kIwStages][kIwTok][kIwDyLd];
-  __shared__ __align__(128) __half s_w[kIwStages][kIwRows][CT + 8];
+  extern __shared__ __align__(1024) unsigned char smem[];
+  auto s_dy = reinterpret_cast<__half (*)[kIwTok][kIwDyLd]>(smem);
+  auto s_w = reinterpret_cast<__half (*)[kIwRows][CT + 8]>(s_dy + kIwStages);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the packed product runs beside this
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int l = (int)blockIdx.y >= a.ctiles0;
@@ -784,17 +792,17 @@ __global__ void __launch_bounds__(kIwThreads) k_gated_igw(const __grid_constant_
   const int mb = blockIdx.x * kIwTok, t0 = ((int)blockIdx.y - (l ? a.ctiles0 : 0)) * CT;
   const int i_lo = blockIdx.z * a.per, i_hi = min(a.N, i_lo + a.per);
   const int nchunk = max(0, (i_hi - i_lo + kIwRows - 1) / kIwRows);
-  auto load = [&](int c, int st) {   // rows i_lo + 32 c .. of this split into stage st
+  auto load = [&](int c, int st) {   // rows i_lo + 64 c .. of this split into stage st
     const int ib = i_lo + c * kIwRows;
     #pragma unroll
-    for (int u = 0; u < 2; ++u) {    // dY: 64 tokens x 4 pieces of 8 rows (rows N .. ldy - 1 hold zeros)
-      const int e = tid + u * kIwThreads, m = e >> 2, pc = e & 3;
+    for (int u = 0; u < kIwTok * kIwRows / 8 / kIwThreads; ++u) {   // dY: 8-row pieces (rows N .. ldy - 1 hold zeros)
+      const int e = tid + u * kIwThreads, m = e / (kIwRows / 8), pc = e % (kIwRows / 8);
       const int mm = mb + m, row = ib + pc * 8;
       const bool ok = mm < a.M && row < i_hi;
       cp_async16(&s_dy[st][m][pc * 8], dy + (ok ? (size_t)mm * a.ldy + row : 0), ok);
     }
     #pragma unroll
-    for (int u = 0; u < CT / 32; ++u) {   // weak block: 32 rows x CT / 8 pieces of 8 slots
+    for (int u = 0; u < kIwRows * CT / 8 / kIwThreads; ++u) {       // weak block: CT / 8 pieces of 8 slots a row
       const int e = tid + u * kIwThreads, r = e / (CT / 8), pc = e % (CT / 8), row = ib + r, col = t0 + pc * 8;
       const bool ok = row < i_hi && col < k_ld;
       cp_async16(&s_w[st][r][pc * 8], w + (ok ? (size_t)row * k_ld + col : 0), ok);
@@ -1024,12 +1032,12 @@ IgPlan ig_plan(const Layer& gate, const Layer& up, int M) {
     f.pad[l] = at;
     if (gate.N % 8) at += up256((size_t)M * f.ldy * sizeof(__half));
   }
-  // weak products: about two CTAs per SM; at least 4 chunks of 32 rows and at most kIwMaxSplits
-  // splits (the input gradient's epilogue adds them)
+  // weak products: up to three CTAs per SM; at least 4 chunks of rows and at most kIwMaxSplits splits
+  // (the input gradient's epilogue adds them)
   f.ct = std::max(gate.k, up.k) > 32 ? 64 : 32;
   const int R = (M + kIwTok - 1) / kIwTok, C = (gate.k + f.ct - 1) / f.ct + (up.k + f.ct - 1) / f.ct;
   const int nch = (gate.N + kIwRows - 1) / kIwRows;
-  f.wsplits = C > 0 ? std::max(1, std::min({(2 * sms + R * C - 1) / (R * C), nch / 4, kIwMaxSplits})) : 1;
+  f.wsplits = C > 0 ? std::max(1, std::min({3 * sms / (R * C), nch / 4, kIwMaxSplits})) : 1;
   f.wper = (nch + f.wsplits - 1) / f.wsplits;
   f.wsplits = (nch + f.wper - 1) / f.wper;
   f.wper *= kIwRows;
@@ -1040,6 +1048,16 @@ IgPlan ig_plan(const Layer& gate, const Layer& up, int M) {
   f.ws = at;
   f.total = at + partial_bytes(f.split, f.BN);
   return f;
+}
+
+template <int CT>
+cudaError_t launch_igw(const GatedIgwArgs& a, dim3 grid, int device, cudaStream_t s) {
+  static std::atomic<unsigned long long> allowed{0};
+  constexpr int smem = igw_smem_bytes<CT>();
+  const cudaError_t e = allow_smem((const void*)k_gated_igw<CT>, smem, device, allowed);
+  if (e != cudaSuccess) return e;
+  k_gated_igw<CT><<<grid, kIwThreads, smem, s>>>(a);
+  return cudaGetLastError();
 }
 
 template <int BITS, int BN>
@@ -1094,9 +1112,11 @@ owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const 
   }
   if (C > 0) {
     const dim3 grid((M + kIwTok - 1) / kIwTok, C, f.wsplits);
-    if (f.ct == 64) k_gated_igw<64><<<grid, kIwThreads, 0, s>>>(wa);
-    else k_gated_igw<32><<<grid, kIwThreads, 0, s>>>(wa);
-    if (cudaGetLastError() != cudaSuccess) return OWQ_ERR_CUDA;
+    const cudaError_t e = f.ct == 64 ? launch_igw<64>(wa, grid, gate.device, s) : launch_igw<32>(wa, grid, gate.device, s);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return OWQ_ERR_CUDA;
+    }
   }
   // beside the weak products: only the epilogues of blocks with weak columns wait for them
   void* args[] = {&maps, &prm};
