@@ -54,7 +54,7 @@ constexpr int ring_smem_bytes() { return Stage<BITS, BN>::kS * Stage<BITS, BN>::
 // ceil(T / P) tile times, with the last T mod P of them split over the idle pairs about T / P.
 struct TileSplit {
   int tiles, whole, splits, steps;
-  int pairs() const { return whole + (tiles - whole) * splits; }
+  __host__ __device__ int pairs() const { return whole + (tiles - whole) * splits; }
 };
 struct TileOf {   // a pair's part
   int tile, split, n_splits, first, steps;
@@ -153,6 +153,9 @@ __device__ __forceinline__ void gated_epilogue(const GatedGemmParams& p, uint32_
 // A cluster of two CTAs computes 256 MMA rows x BN tokens with cta_group::2: each CTA unpacks its
 // own 128 rows and holds half of the tokens, which halves the activations' traffic from L2 (at 256
 // tokens a lone CTA would want 64 KB a step, 17 TB/s over the GPU) and their room in the ring.
+// Persistent: a pair takes the parts pair, pair + P, ... (P pairs in the grid), its rings running on
+// across them.  The loads of the next part, and its first kS2 steps of A operand, are under way while
+// the last products of this one run and its epilogue drains the accumulator.
 //   warp 0      TMA producer of the CTA's ring (freed by the MMAs' commit in both CTAs)
 //   warp 1      tensor memory; in the even CTA the MMA-issuing thread
 //   warps 2-17  A operand, in kGR groups on alternate steps: wait for the stage's loads, unpack, store
@@ -169,17 +172,24 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
   uint64_t* full = bars;              // [S] TMA landed
   uint64_t* empty = bars + S;         // [S] MMAs of the stage done
   uint64_t* afull = bars + 2 * S;     // [kS2] A stage written in both CTAs (the even CTA's is used)
-  uint64_t* accf = bars + 2 * S + kS2;   // accumulator complete
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + kS2 + 1);
+  uint64_t* accf = bars + 2 * S + kS2;       // accumulator complete
+  uint64_t* acce = bars + 2 * S + kS2 + 1;   // accumulator read out by both CTAs (the even CTA's is used)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + kS2 + 2);
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (warp: uniform)
   const int rank = (int)cluster_ctarank();
-  const TileOf to = tile_of(p.split, blockIdx.x >> 1, p.K / kStepCodes);
-  const int n0 = ((to.tile % p.rts) * 2 + rank) * kHalfRows;   // first output row of this CTA
-  const int m0 = (to.tile / p.rts) * BN;                       // first token
-  const int kb0 = to.first, nD = to.steps;        // dense steps of this split
-  const int nK = nD + (to.split == to.n_splits - 1 ? p.nw : 0);   // + the weak steps (last split)
+  const int first_part = blockIdx.x >> 1, P = gridDim.x >> 1, parts = p.split.pairs();
+  const int all_steps = p.K / kStepCodes;
+  auto steps_of = [&](const TileOf& t) { return t.steps + (t.split == t.n_splits - 1 ? p.nw : 0); };   // + the weak steps (last split)
+  auto row0_of = [&](const TileOf& t) { return ((t.tile % p.rts) * 2 + rank) * kHalfRows; };   // first output row of this CTA
+  auto token0_of = [&](const TileOf& t) { return t.tile / p.rts * BN; };
   const bool per_group = p.G > 1;
+  TileOf to = tile_of(p.split, first_part, all_steps);   // the part at hand
+  int nK = steps_of(to), n0 = row0_of(to), m0 = token0_of(to);
+  auto next = [&](int part) {
+    to = tile_of(p.split, part, all_steps);
+    nK = steps_of(to); n0 = row0_of(to); m0 = token0_of(to);
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -188,6 +198,7 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
     }
     for (int s = 0; s < kS2; ++s) mbar_init(&afull[s], 2 * kDW / kGR);   // a lane of each warp, both CTAs
     mbar_init(accf, 1);
+    mbar_init(acce, 2 * kDW);
     fence_mbar_init();
     prefetch_tmap(&maps.x);
     prefetch_tmap(&maps.p[0]);
@@ -205,35 +216,40 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
     if (lane == 0) {
       // ---------------- TMA producer ----------------
       const uint32_t kDense = L::kX + L::kP + (per_group ? L::kSZ : 0);
-      const int mt = m0 + rank * (BN / 2);   // this CTA's tokens
-      bool ok = true;
-      int issued = 0;
-      for (int i = 0; i < nK && ok; ++i) {
-        const int s = i % S, u = i / S;
-        if (u > 0) ok = mbar_wait(&empty[s], (u - 1) & 1, p.status, p.wait_limit);
-        if (!ok) break;
-        unsigned char* st = smem + s * L::kBytes;
-        if (i < nD) {
-          const int kb = kb0 + i;
-          mbar_arrive_expect_tx(&full[s], kDense);
-          #pragma unroll
-          for (int l = 0; l < 2; ++l) {
-            tma_load_3d(st + L::kX + l * (L::kP / 2), &maps.p[l], &full[s], 0, kb, n0 / 16);
-            if (per_group) tma_load_3d(st + L::kX + L::kP + l * (L::kSZ / 2), &maps.sz[l], &full[s], 0, kb, n0 / 16);
+      bool ok = true, waited = false;
+      int g = 0;   // steps issued
+      for (int part = first_part; ok;) {
+        const int n16 = n0 / 16, mt = m0 + rank * (BN / 2);   // mt: this CTA's tokens
+        for (int i = 0; i < nK; ++i) {
+          const int s = g % S, u = g / S;
+          if (u > 0) ok = mbar_wait(&empty[s], (u - 1) & 1, p.status, p.wait_limit);
+          if (!ok) break;
+          unsigned char* st = smem + s * L::kBytes;
+          if (i < to.steps) {
+            const int kb = to.first + i;
+            mbar_arrive_expect_tx(&full[s], kDense);
+            #pragma unroll
+            for (int l = 0; l < 2; ++l) {
+              tma_load_3d(st + L::kX + l * (L::kP / 2), &maps.p[l], &full[s], 0, kb, n16);
+              if (per_group) tma_load_3d(st + L::kX + L::kP + l * (L::kSZ / 2), &maps.sz[l], &full[s], 0, kb, n16);
+            }
+            tma_load_2d(st, &maps.x, &full[s], kb * kStepCodes, mt);
+            tma_load_2d(st + BN * 64, &maps.x, &full[s], kb * kStepCodes + 64, mt);
+          } else {
+            const int c0 = (i - to.steps) * 64;
+            if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");   // the gathered activations
+            waited = true;
+            mbar_arrive_expect_tx(&full[s], L::kX);
+            tma_load_2d(st, &maps.xw[0], &full[s], c0, mt);
+            tma_load_2d(st + BN * 64, &maps.xw[1], &full[s], c0, mt);
           }
-          tma_load_2d(st, &maps.x, &full[s], kb * kStepCodes, mt);
-          tma_load_2d(st + BN * 64, &maps.x, &full[s], kb * kStepCodes + 64, mt);
-        } else {
-          const int c0 = (i - nD) * 64;
-          if (i == nD) asm volatile("griddepcontrol.wait;" ::: "memory");   // the gathered activations
-          mbar_arrive_expect_tx(&full[s], L::kX);
-          tma_load_2d(st, &maps.xw[0], &full[s], c0, mt);
-          tma_load_2d(st + BN * 64, &maps.xw[1], &full[s], c0, mt);
+          ++g;
         }
-        issued = i + 1;
+        if ((part += P) >= parts) break;
+        next(part);
       }
       // never leave with copies in flight: wait for the last issued use of every stage
-      for (int i = (issued > S ? issued - S : 0); i < issued; ++i)
+      for (int i = (g > S ? g - S : 0); i < g; ++i)
         mbar_wait(&full[i % S], (i / S) & 1, p.status, p.wait_limit);
     }
   } else if (warp == 1) {
@@ -243,32 +259,39 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
       constexpr uint32_t idesc = idesc_f16_f32(2 * kBM, BN);
       const uint64_t dbase = desc_sw128_kmajor(smem_u32(smem));
       bool ok = true;
-      int s = 0;
-      for (int i = 0; i < nK && ok; ++i) {
-        ok = mbar_wait(&afull[i % kS2], (i / kS2) & 1, p.status, p.wait_limit);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t ds = dbase + (uint64_t)((s * L::kBytes) >> 4);
-          const uint32_t at = tmem + BN + 64 * (i % kS2);
-          if (i < nD) {
-            mma_f16_ts_pair(tmem, at, ds, idesc, i != 0);
-            #pragma unroll
-            for (int kk = 1; kk < 8; ++kk)
-              mma_f16_ts_pair(tmem, at + 8 * kk, ds + (uint64_t)((((kk >> 2) * BN * 64) + (kk & 3) * 32) >> 4), idesc, 1u);
-          } else {   // only the slices that hold weak columns
-            #pragma unroll 1
-            for (int kk = 0; kk < 8; ++kk)
-              if ((i - nD) * 64 + (kk & 3) * 16 < p.k_ld[kk >> 2])
+      int s = 0, g = 0, it = 0;
+      for (int part = first_part; ok; ++it) {
+        const int nD = to.steps;
+        for (int i = 0; i < nK; ++i, ++g) {
+          ok = mbar_wait(&afull[g % kS2], (g / kS2) & 1, p.status, p.wait_limit);
+          if (i == 0 && it > 0) ok = mbar_wait(acce, (it - 1) & 1, p.status, p.wait_limit) && ok;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t ds = dbase + (uint64_t)((s * L::kBytes) >> 4);
+            const uint32_t at = tmem + BN + 64 * (g % kS2);
+            if (i < nD) {
+              mma_f16_ts_pair(tmem, at, ds, idesc, i != 0);
+              #pragma unroll
+              for (int kk = 1; kk < 8; ++kk)
                 mma_f16_ts_pair(tmem, at + 8 * kk, ds + (uint64_t)((((kk >> 2) * BN * 64) + (kk & 3) * 32) >> 4), idesc, 1u);
+            } else {   // only the slices that hold weak columns
+              #pragma unroll 1
+              for (int kk = 0; kk < 8; ++kk)
+                if ((i - nD) * 64 + (kk & 3) * 16 < p.k_ld[kk >> 2])
+                  mma_f16_ts_pair(tmem, at + 8 * kk, ds + (uint64_t)((((kk >> 2) * BN * 64) + (kk & 3) * 32) >> 4), idesc, 1u);
+            }
+            mma_commit_pair(&empty[s]);
           }
-          mma_commit_pair(&empty[s]);
+          __syncwarp();
+          if (++s == S) s = 0;
         }
+        if (elect_one()) mma_commit_pair(accf);
         __syncwarp();
-        if (++s == S) s = 0;
+        if ((part += P) >= parts) break;
+        next(part);
       }
-      if (elect_one()) mma_commit_pair(accf);
     }
   } else {
     // ---------------- A operand ----------------
@@ -277,22 +300,78 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
     constexpr int NSL = kDW / kGR / 4, U = 16 / NSL;
     const int quarter = warp & 3, aw = warp - 2, grp = aw / (kDW / kGR), jh = (aw % (kDW / kGR)) >> 2;
     const int lay = lane >> 4, tr = 16 * quarter + (lane & 15);   // layer and row of the tile
-    const int orow = n0 + tr;
-    const int row = min(orow, p.N - 1);
     const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
+    constexpr int kCols = BN / (kDW / 4);   // accumulator columns of this warp in the epilogue
+    const int col0 = (aw >> 2) * kCols;
+    const uint32_t acc = tmem + lane_base + (uint32_t)col0;
     RowDq<BITS> dq;
-    if (!per_group)
+    int part = first_part, g0 = 0, i = grp, it = 0;   // g0: the part's first step, over all parts
+    int orow = n0 + tr, row = min(orow, p.N - 1);
+    auto channel = [&]() {
       dq.set((uint32_t)__half_as_ushort(p.scales[lay][row]) | (uint32_t)__half_as_ushort(p.zeros[lay][row]) << 16);
+    };
+    if (!per_group) channel();
+    TileOf ep = to;   // the part before, and this thread's output row in it
+    int erow = orow, em0 = m0;
     bool ok = true;
-    for (int i = grp; i < nK && ok; i += kGR) {
-      const int s = i % S, u = i / S;
+    while (true) {
+      const bool more = part < parts;
+      if (it > 0 && (!more || i >= min(kS2, nK))) {
+        // ---------------- epilogue of the part before (`it`: parts whose A operand is written, negated after it) ----------------
+        auto wait = [&]() {
+          const bool acc_ok = __all_sync(0xffffffffu, mbar_wait(accf, (it - 1) & 1, p.status, p.wait_limit));
+          tc_fence_after();
+          return acc_ok;
+        };
+        if (ep.n_splits > 1) {   // this split's fp32 partials
+          const bool acc_ok = wait();
+          float* w = p.ws + partial_at(p.split, ep.split, ep.tile, rank, BN) + (size_t)col0 * kBM + 32 * quarter + lane;
+          #pragma unroll 1
+          for (int c = 0; c < kCols && acc_ok; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(acc + (uint32_t)c, v);
+            tmem_ld_wait();
+            #pragma unroll
+            for (int j = 0; j < 16; ++j) w[(size_t)(c + j) * kBM] = __uint_as_float(v[j]);
+          }
+        } else {
+          with_act(p.act, [&](auto act) {
+            constexpr int A = decltype(act)::value;
+            const int first = em0 + col0 + 8 * lay;
+            if (p.dh) gated_epilogue<A, true, kCols>(p, acc, first, erow, lay, wait);
+            else gated_epilogue<A, false, kCols>(p, acc, first, erow, lay, wait);
+          });
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(acce, 0);
+        it = -it;
+      }
+      if (!more) break;
+      if (i >= nK) {   // the next part
+        g0 += nK;
+        i -= nK;
+        it = (it < 0 ? -it : it) + 1;
+        part += P;
+        ep = to;
+        erow = orow;
+        em0 = m0;
+        if (part < parts) {
+          next(part);
+          orow = n0 + tr;
+          row = min(orow, p.N - 1);
+          if (!per_group) channel();
+        }
+        continue;
+      }
+      const int g = g0 + i, s = g % S, u = g / S, nD = to.steps;
       ok = mbar_wait(&full[s], u & 1, p.status, p.wait_limit);
-      if (i >= kS2) ok = mbar_wait(&empty[(i - kS2) % S], ((i - kS2) / S) & 1, p.status, p.wait_limit) && ok;   // the A stage's MMAs
+      if (g >= kS2) ok = mbar_wait(&empty[(g - kS2) % S], ((g - kS2) / S) & 1, p.status, p.wait_limit) && ok;   // the A stage's MMAs
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       const unsigned char* st = smem + s * L::kBytes;
-      const uint32_t at = tmem + lane_base + BN + 64 * (i % kS2) + 4 * U * jh;
+      const uint32_t at = tmem + lane_base + BN + 64 * (g % kS2) + 4 * U * jh;
       uint32_t d[U / 4][16];
       if (i < nD) {
         if (per_group) dq.set(*reinterpret_cast<const uint32_t*>(st + L::kX + L::kP + lay * (L::kSZ / 2) + tr * 4));
@@ -338,36 +417,8 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0 && !(p.skip_arrive && i == 0 && threadIdx.x == 64)) mbar_arrive_remote(&afull[i % kS2], 0);
-    }
-
-    // ---------------- epilogue ----------------
-    constexpr int kCols = BN / (kDW / 4);   // accumulator columns of this warp
-    const int col0 = (aw >> 2) * kCols;
-    const uint32_t acc = tmem + lane_base + (uint32_t)col0;
-    auto wait = [&]() {
-      const bool acc_ok = __all_sync(0xffffffffu, mbar_wait(accf, 0, p.status, p.wait_limit) && ok);
-      tc_fence_after();
-      return acc_ok;
-    };
-    if (to.n_splits > 1) {   // this split's fp32 partials
-      const bool acc_ok = wait();
-      float* w = p.ws + partial_at(p.split, to.split, to.tile, rank, BN) + (size_t)col0 * kBM + 32 * quarter + lane;
-      #pragma unroll 1
-      for (int c = 0; c < kCols && acc_ok; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(acc + (uint32_t)c, v);
-        tmem_ld_wait();
-        #pragma unroll
-        for (int j = 0; j < 16; ++j) w[(size_t)(c + j) * kBM] = __uint_as_float(v[j]);
-      }
-    } else {
-      with_act(p.act, [&](auto act) {
-        constexpr int A = decltype(act)::value;
-        const int first = m0 + col0 + 8 * lay;
-        if (p.dh) gated_epilogue<A, true, kCols>(p, acc, first, orow, lay, wait);
-        else gated_epilogue<A, false, kCols>(p, acc, first, orow, lay, wait);
-      });
+      if (lane == 0 && !(p.skip_arrive && g == 0 && threadIdx.x == 64)) mbar_arrive_remote(&afull[g % kS2], 0);
+      i += kGR;
     }
   }
 
@@ -987,7 +1038,7 @@ owq_status_t run_gemm(const Layer& gate, const Layer& up, int act, const __half*
   }
   // beside the gather: only the weak steps wait for it
   void* args[] = {&maps, &prm};
-  if (launch_pdl((void*)kern, dim3(2 * f.split.pairs()), 32 * (2 + kDW), smem, ld > 0, s, args) != cudaSuccess) {
+  if (launch_pdl((void*)kern, dim3(2 * std::min(f.split.pairs(), layer_sm_count(gate.device) / 2)), 32 * (2 + kDW), smem, ld > 0, s, args) != cudaSuccess) {
     cudaGetLastError();
     allowed = 0;
     return OWQ_ERR_CUDA;
