@@ -30,7 +30,7 @@ constexpr int kDW = 16;                // A-operand warps
 constexpr int kGR = 2;                 // groups of them, on alternate steps
 constexpr uint32_t kTmemCols = 512;    // the accumulator (BN columns), then the A stages of 64 columns
 template <int BN>
-constexpr int a_stages() { return BN == 256 ? 4 : 6; }
+constexpr int a_stages() { return BN == 256 ? 4 : BN == 192 ? 5 : 6; }
 
 // One ring stage of a CTA: half of the step's tokens (two 128B-swizzled boxes of 64 columns), the
 // packed block of its 128 rows and their (scale, zero) pairs.
@@ -213,20 +213,27 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer ----------------
-      const uint32_t kDense = L::kX + L::kP + (per_group ? L::kSZ : 0);
-      bool ok = true, waited = false;
-      int g = 0;   // steps issued
-      for (int part = first_part; ok;) {
-        const int n16 = n0 / 16, mt = m0 + rank * (BN / 2);   // mt: this CTA's tokens
-        for (int i = 0; i < nK; ++i) {
-          const int s = g % S, u = g / S;
-          if (u > 0) ok = mbar_wait(&empty[s], (u - 1) & 1, p.status, p.wait_limit);
-          if (!ok) break;
-          unsigned char* st = smem + s * L::kBytes;
-          if (i < to.steps) {
-            const int kb = to.first + i;
+    // ---------------- TMA producer ----------------
+    // The whole warp runs the loop and one lane issues, so that the copies' operands stay in uniform
+    // registers (values that a lone lane carries from part to part do not: 0.55 instead of 0.46 us a
+    // step at 64 tokens).
+    const uint32_t kDense = L::kX + L::kP + (per_group ? L::kSZ : 0);
+    bool ok = true, waited = false;
+    int s = 0, ph = 1, g = 0;   // ring stage, phase of its `empty`, steps issued
+    for (int part = first_part; ok;) {
+      const int n16 = __shfl_sync(0xffffffffu, n0 / 16, 0), mt = __shfl_sync(0xffffffffu, m0, 0) + rank * (BN / 2);   // mt: this CTA's tokens
+      const int steps = __shfl_sync(0xffffffffu, nK, 0), nD = __shfl_sync(0xffffffffu, to.steps, 0), kb0 = __shfl_sync(0xffffffffu, to.first, 0);
+      for (int i = 0; i < steps; ++i) {
+        if (g >= S) ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ph, p.status, p.wait_limit));
+        if (!ok) break;
+        unsigned char* st = smem + s * L::kBytes;
+        if (i >= nD && !waited) {
+          asm volatile("griddepcontrol.wait;" ::: "memory");   // the gathered activations
+          waited = true;
+        }
+        if (elect_one()) {
+          if (i < nD) {
+            const int kb = kb0 + i;
             mbar_arrive_expect_tx(&full[s], kDense);
             #pragma unroll
             for (int l = 0; l < 2; ++l) {
@@ -236,22 +243,22 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
             tma_load_2d(st, &maps.x, &full[s], kb * kStepCodes, mt);
             tma_load_2d(st + BN * 64, &maps.x, &full[s], kb * kStepCodes + 64, mt);
           } else {
-            const int c0 = (i - to.steps) * 64;
-            if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");   // the gathered activations
-            waited = true;
+            const int c0 = (i - nD) * 64;
             mbar_arrive_expect_tx(&full[s], L::kX);
             tma_load_2d(st, &maps.xw[0], &full[s], c0, mt);
             tma_load_2d(st + BN * 64, &maps.xw[1], &full[s], c0, mt);
           }
-          ++g;
         }
-        if ((part += P) >= parts) break;
-        next(part);
+        __syncwarp();
+        ++g;
+        if (++s == S) { s = 0; ph ^= 1; }
       }
-      // never leave with copies in flight: wait for the last issued use of every stage
-      for (int i = (g > S ? g - S : 0); i < g; ++i)
-        mbar_wait(&full[i % S], (i / S) & 1, p.status, p.wait_limit);
+      if ((part += P) >= parts) break;
+      next(part);
     }
+    // never leave with copies in flight: wait for the last issued use of every stage
+    for (int i = (g > S ? g - S : 0); i < g; ++i)
+      mbar_wait(&full[i % S], (i / S) & 1, p.status, p.wait_limit);
   } else if (warp == 1) {
     if (rank == 0) {   // the whole warp runs the loop, so that its values stay in uniform registers
       // ---------------- MMA issuer ----------------
@@ -259,18 +266,18 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
       constexpr uint32_t idesc = idesc_f16_f32(2 * kBM, BN);
       const uint64_t dbase = desc_sw128_kmajor(smem_u32(smem));
       bool ok = true;
-      int s = 0, g = 0, it = 0;
-      for (int part = first_part; ok; ++it) {
-        const int nD = to.steps;
-        for (int i = 0; i < nK; ++i, ++g) {
-          ok = mbar_wait(&afull[g % kS2], (g / kS2) & 1, p.status, p.wait_limit);
-          if (i == 0 && it > 0) ok = mbar_wait(acce, (it - 1) & 1, p.status, p.wait_limit) && ok;
+      int s = 0, a = 0, aph = 0;   // ring stage, A stage and its phase
+      for (int part = first_part, it = 0;; ++it) {
+        const int steps = __shfl_sync(0xffffffffu, nK, 0), nD = __shfl_sync(0xffffffffu, to.steps, 0);
+        if (it > 0) ok = __all_sync(0xffffffffu, mbar_wait(acce, (it - 1) & 1, p.status, p.wait_limit));
+        for (int i = 0; i < steps && ok; ++i) {
+          ok = mbar_wait(&afull[a], aph, p.status, p.wait_limit);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
             const uint64_t ds = dbase + (uint64_t)((s * L::kBytes) >> 4);
-            const uint32_t at = tmem + BN + 64 * (g % kS2);
+            const uint32_t at = tmem + BN + 64 * a;
             if (i < nD) {
               mma_f16_ts_pair(tmem, at, ds, idesc, i != 0);
               #pragma unroll
@@ -286,10 +293,11 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
           }
           __syncwarp();
           if (++s == S) s = 0;
+          if (++a == kS2) { a = 0; aph ^= 1; }
         }
         if (elect_one()) mma_commit_pair(accf);
         __syncwarp();
-        if ((part += P) >= parts) break;
+        if (!ok || (part += P) >= parts) break;
         next(part);
       }
     }
@@ -305,19 +313,85 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
     const int col0 = (aw >> 2) * kCols;
     const uint32_t acc = tmem + lane_base + (uint32_t)col0;
     RowDq<BITS> dq;
-    int part = first_part, g0 = 0, i = grp, it = 0;   // g0: the part's first step, over all parts
     int orow = n0 + tr, row = min(orow, p.N - 1);
     auto channel = [&]() {
       dq.set((uint32_t)__half_as_ushort(p.scales[lay][row]) | (uint32_t)__half_as_ushort(p.zeros[lay][row]) << 16);
     };
     if (!per_group) channel();
-    TileOf ep = to;   // the part before, and this thread's output row in it
+    TileOf ep = to;            // the part before, and this thread's output row in it
     int erow = orow, em0 = m0;
-    bool ok = true;
+    int part = first_part, g0 = 0, i = grp, it = 0;   // g0: the part's first step, over all parts; it: parts before it
+    int stop = nK;             // with an epilogue pending: after the steps that run ahead of it
+    bool ok = true, pending = false;
+    const uint32_t ring = smem_u32(smem);
+    auto ready = [&](int g) {   // step g's loads have landed and its A stage's last MMAs are done
+      bool r = mbar_wait(&full[g % S], (g / S) & 1, p.status, p.wait_limit);
+      if (g >= kS2) r = mbar_wait(&empty[(g - kS2) % S], ((g - kS2) / S) & 1, p.status, p.wait_limit) && r;
+      r = __all_sync(0xffffffffu, r);
+      tc_fence_after();
+      return r;
+    };
+    auto put = [&](int g, const uint32_t (&d)[U / 4][16]) {
+      const uint32_t at = tmem + lane_base + BN + 64 * (g % kS2) + 4 * U * jh;
+      #pragma unroll
+      for (int h = 0; h < U / 4; ++h) tmem_st16(at + 16 * h, d[h]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && !(p.skip_arrive && g == 0 && threadIdx.x == 64)) mbar_arrive_remote(&afull[g % kS2], 0);
+    };
     while (true) {
-      const bool more = part < parts;
-      if (it > 0 && (!more || i >= min(kS2, nK))) {
-        // ---------------- epilogue of the part before (`it`: parts whose A operand is written, negated after it) ----------------
+      const int nD = to.steps, dense = min(stop, nD);
+      for (; i < dense && ok; i += kGR) {
+        const int g = g0 + i;
+        if (!(ok = ready(g))) break;
+        const uint32_t st = ring + (g % S) * L::kBytes;
+        if (per_group) dq.set(lds_u1(st + L::kX + L::kP + lay * (L::kSZ / 2) + tr * 4));
+        uint32_t w[4 * BITS], d[U / 4][16];
+        #pragma unroll
+        for (int v = 0; v < BITS; ++v) {
+          const uint4 q = lds_u4(st + L::kX + lay * (L::kP / 2) + tr * 16 * BITS + 16 * v);
+          w[4 * v] = q.x; w[4 * v + 1] = q.y; w[4 * v + 2] = q.z; w[4 * v + 3] = q.w;
+        }
+        auto units = [&](auto sl_c) {
+          constexpr int SL = decltype(sl_c)::value;
+          #pragma unroll
+          for (int ju = 0; ju < U; ++ju)
+            #pragma unroll
+            for (int q = 0; q < 4; ++q)
+              d[ju >> 2][4 * (ju & 3) + q] = dequant<BITS>(w + q * BITS, U * SL + ju, dq);
+        };
+        if constexpr (NSL == 2) {
+          if (jh == 0) units(std::integral_constant<int, 0>{});
+          else units(std::integral_constant<int, 1>{});
+        } else {
+          switch (jh) {
+            case 0: units(std::integral_constant<int, 0>{}); break;
+            case 1: units(std::integral_constant<int, 1>{}); break;
+            case 2: units(std::integral_constant<int, 2>{}); break;
+            default: units(std::integral_constant<int, 3>{}); break;
+          }
+        }
+        put(g, d);
+      }
+      #pragma unroll 1
+      for (; i < stop && ok; i += kGR) {
+        // weak step: slab jh covers columns c0 .. c0 + 8 U - 1 of layer wl's part of the step
+        const int g = g0 + i, wl = (8 * U * jh) / 64, c0 = (i - nD) * 64 + (8 * U * jh) % 64;
+        if (!(ok = ready(g))) break;
+        const uint4* src = reinterpret_cast<const uint4*>(p.w_weak[lay] + (size_t)row * p.k_ld[lay] + c0);
+        uint32_t d[U / 4][16];
+        #pragma unroll
+        for (int v = 0; v < U; ++v) {
+          const uint4 q = (lay == wl && orow < p.N && c0 + 8 * v < p.k_ld[lay]) ? src[v] : make_uint4(0, 0, 0, 0);
+          d[v >> 2][4 * (v & 3)] = q.x; d[v >> 2][4 * (v & 3) + 1] = q.y;
+          d[v >> 2][4 * (v & 3) + 2] = q.z; d[v >> 2][4 * (v & 3) + 3] = q.w;
+        }
+        put(g, d);
+      }
+      if (!ok) break;
+      if (pending) {
+        // ---------------- epilogue of the part before ----------------
         auto wait = [&]() {
           const bool acc_ok = __all_sync(0xffffffffu, mbar_wait(accf, (it - 1) & 1, p.status, p.wait_limit));
           tc_fence_after();
@@ -345,80 +419,27 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(acce, 0);
-        it = -it;
-      }
-      if (!more) break;
-      if (i >= nK) {   // the next part
+        if (part >= parts) break;
+        pending = false;
+        stop = nK;
+      } else {   // the next part
+        pending = true;
         g0 += nK;
         i -= nK;
-        it = (it < 0 ? -it : it) + 1;
+        ++it;
         part += P;
         ep = to;
         erow = orow;
         em0 = m0;
+        stop = i;
         if (part < parts) {
           next(part);
           orow = n0 + tr;
           row = min(orow, p.N - 1);
           if (!per_group) channel();
-        }
-        continue;
-      }
-      const int g = g0 + i, s = g % S, u = g / S, nD = to.steps;
-      ok = mbar_wait(&full[s], u & 1, p.status, p.wait_limit);
-      if (g >= kS2) ok = mbar_wait(&empty[(g - kS2) % S], ((g - kS2) / S) & 1, p.status, p.wait_limit) && ok;   // the A stage's MMAs
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const unsigned char* st = smem + s * L::kBytes;
-      const uint32_t at = tmem + lane_base + BN + 64 * (g % kS2) + 4 * U * jh;
-      uint32_t d[U / 4][16];
-      if (i < nD) {
-        if (per_group) dq.set(*reinterpret_cast<const uint32_t*>(st + L::kX + L::kP + lay * (L::kSZ / 2) + tr * 4));
-        const uint4* pw = reinterpret_cast<const uint4*>(st + L::kX + lay * (L::kP / 2) + tr * 16 * BITS);
-        uint32_t w[4 * BITS];
-        #pragma unroll
-        for (int v = 0; v < BITS; ++v) {
-          const uint4 q = pw[v];
-          w[4 * v] = q.x; w[4 * v + 1] = q.y; w[4 * v + 2] = q.z; w[4 * v + 3] = q.w;
-        }
-        auto units = [&](auto sl_c) {
-          constexpr int SL = decltype(sl_c)::value;
-          #pragma unroll
-          for (int ju = 0; ju < U; ++ju)
-            #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              d[ju >> 2][4 * (ju & 3) + q] = dequant<BITS>(w + q * BITS, U * SL + ju, dq);
-        };
-        if constexpr (NSL == 2) {
-          if (jh == 0) units(std::integral_constant<int, 0>{});
-          else units(std::integral_constant<int, 1>{});
-        } else {
-          switch (jh) {
-            case 0: units(std::integral_constant<int, 0>{}); break;
-            case 1: units(std::integral_constant<int, 1>{}); break;
-            case 2: units(std::integral_constant<int, 2>{}); break;
-            default: units(std::integral_constant<int, 3>{}); break;
-          }
-        }
-      } else {
-        // weak step: slab jh covers columns c0 .. c0 + 8 U - 1 of layer wl's part of the step
-        const int wl = (8 * U * jh) / 64, c0 = (i - nD) * 64 + (8 * U * jh) % 64;
-        const uint4* src = reinterpret_cast<const uint4*>(p.w_weak[lay] + (size_t)row * p.k_ld[lay] + c0);
-        #pragma unroll
-        for (int v = 0; v < U; ++v) {
-          const uint4 q = (lay == wl && orow < p.N && c0 + 8 * v < p.k_ld[lay]) ? src[v] : make_uint4(0, 0, 0, 0);
-          d[v >> 2][4 * (v & 3)] = q.x; d[v >> 2][4 * (v & 3) + 1] = q.y;
-          d[v >> 2][4 * (v & 3) + 2] = q.z; d[v >> 2][4 * (v & 3) + 3] = q.w;
+          stop = min(kS2, nK);
         }
       }
-      #pragma unroll
-      for (int h = 0; h < U / 4; ++h) tmem_st16(at + 16 * h, d[h]);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0 && !(p.skip_arrive && g == 0 && threadIdx.x == 64)) mbar_arrive_remote(&afull[g % kS2], 0);
-      i += kGR;
     }
   }
 
@@ -523,11 +544,6 @@ __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_
   asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
                :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
-}
-__device__ __forceinline__ uint32_t lds_u1(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
 }
 
 // The words of a chunk that its pairs 4 Q .. 4 Q + 3 (columns 32 Q .. 32 Q + 31 of the block) use
@@ -922,7 +938,7 @@ unsigned blocks_for(size_t n, int threads, unsigned most) {
 
 // Tokens of a tile.  A tile's time is set by forming the A operand up to about 128 tokens and by
 // the MMAs above, so one wide tile beats two narrower ones.
-int gated_tile_tokens(int M) { return M <= 64 ? 64 : M <= 128 ? 128 : 256; }
+int gated_tile_tokens(int M) { return M <= 64 ? 64 : M <= 128 ? 128 : M <= 192 ? 192 : 256; }
 
 // The split of T tiles of `steps` steps over the SM pairs (see TileSplit): at least 4 steps a split, and
 // only where the saved time, in units of a step (about 0.3 us for 64 tokens to 0.65 us for 256),
@@ -1060,6 +1076,7 @@ owq_status_t dispatch_gemm(const Layer& gate, const Layer& up, int act, const __
                            __half* out1, int M, const FwdPlan& f, unsigned char* ws, long long wl, bool skip, cudaStream_t s) {
   switch (f.BN) {
     case 64: return run_gemm<BITS, 64>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
+    case 192: return run_gemm<BITS, 192>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
     case 128: return run_gemm<BITS, 128>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
     default: return run_gemm<BITS, 256>(gate, up, act, x, dh, out0, out1, M, f, ws, wl, skip, s);
   }
@@ -1193,6 +1210,7 @@ owq_status_t dispatch_ig(const Layer& gate, const Layer& up, const __half* dg, c
                          unsigned char* ws, long long wl, cudaStream_t s) {
   switch (f.BN) {
     case 64: return run_ig<BITS, 64>(gate, up, dg, du, dx, M, f, ws, wl, s);
+    case 192: return run_ig<BITS, 192>(gate, up, dg, du, dx, M, f, ws, wl, s);
     case 128: return run_ig<BITS, 128>(gate, up, dg, du, dx, M, f, ws, wl, s);
     default: return run_ig<BITS, 256>(gate, up, dg, du, dx, M, f, ws, wl, s);
   }

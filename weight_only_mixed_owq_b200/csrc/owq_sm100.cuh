@@ -100,6 +100,11 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 
 // ---- explicit shared-memory accesses (32-bit shared addresses; pointers that went through an
 // integer for alignment would otherwise become generic loads) ----
+__device__ __forceinline__ uint32_t lds_u1(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint2 lds_u2(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
