@@ -210,7 +210,7 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
   __syncthreads();
   cluster_sync();   // both CTAs' barriers and tensor memory are ready
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -627,30 +627,31 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
   __syncthreads();
   cluster_sync();   // both CTAs' barriers and tensor memory are ready
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer ----------------
-      const int mt = m0 + rank * (BN / 2);   // this CTA's tokens
-      bool ok = true;
-      int issued = 0;
-      for (int i = 0; i < nK && ok; ++i) {
-        const int s = i % S, u = i / S;
-        if (u > 0) ok = mbar_wait(&empty[s], (u - 1) & 1, p.status, p.wait_limit);
-        if (!ok) break;
-        unsigned char* st = smem + s * L::kBytes;
-        const int l = to.first + i >= nR, rb = to.first + i - (l ? nR : 0);
+    // ---------------- TMA producer (the whole warp, as in the forward product) ----------------
+    const int mt = m0 + rank * (BN / 2);   // this CTA's tokens
+    bool ok = true;
+    int s = 0, ph = 1, i = 0;   // ring stage, phase of its `empty`, steps issued
+    for (; i < nK; ++i) {
+      if (i >= S) ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ph, p.status, p.wait_limit));
+      if (!ok) break;
+      unsigned char* st = smem + s * L::kBytes;
+      const int l = to.first + i >= nR, rb = to.first + i - (l ? nR : 0);
+      if (elect_one()) {
         mbar_arrive_expect_tx(&full[s], L::kX + L::kP + L::kSZ);
         tma_load_3d(st + L::kX, &maps.p[l], &full[s], 0, b, rb * 8);
         tma_load_3d(st + L::kX + L::kP, &maps.sz[l], &full[s], 0, grp, rb * 8);
         tma_load_2d(st, &maps.dy[l], &full[s], rb * 128, mt);
         tma_load_2d(st + BN * 64, &maps.dy[l], &full[s], rb * 128 + 64, mt);
-        issued = i + 1;
       }
-      for (int i = (issued > S ? issued - S : 0); i < issued; ++i)
-        mbar_wait(&full[i % S], (i / S) & 1, p.status, p.wait_limit);
+      __syncwarp();
+      if (++s == S) { s = 0; ph ^= 1; }
     }
+    // never leave with copies in flight: wait for the last issued use of every stage
+    for (int j = (i > S ? i - S : 0); j < i; ++j)
+      mbar_wait(&full[j % S], (j / S) & 1, p.status, p.wait_limit);
   } else if (warp == 1) {
     if (rank == 0) {   // the whole warp runs the loop, so that its values stay in uniform registers
       // ---------------- MMA issuer ----------------
