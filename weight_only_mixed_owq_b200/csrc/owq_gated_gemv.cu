@@ -122,7 +122,8 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
 
   const int lo = min(warp * share, T * U), hi = min(lo + share, T * U);
 
-  // lane 0: the next item of the run into the next stage.  A CTA's blocks of a tile are contiguous.
+  // the next item of the run into the next stage (the whole warp keeps count, one lane issues).  A
+  // CTA's blocks of a tile are contiguous.
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
   int p_lt = lo / U, p_u = lo - p_lt * U, p_left = hi - lo, p_st = 0, in_flight = 0;
@@ -141,11 +142,17 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
     uint64_t* bar = bars + p_st;
     const int cnt = min(min(sub, p_left), U - p_u);
     const uint32_t bytes = (uint32_t)(cnt * U_::kTileBlk), zb = (uint32_t)(cnt * 64);
-    mbar_arrive_expect_tx(bar, 2 * (bytes + (PG ? zb : 0u)));
+    if (elect_one()) {
+      mbar_arrive_expect_tx(bar, 2 * (bytes + (PG ? zb : 0u)));
+      #pragma unroll
+      for (int l = 0; l < 2; ++l) {
+        bulk_load_hint(dst + l * sub * U_::kTileBlk, p_src[l], bytes, bar, pol);
+        if constexpr (PG) bulk_load_hint(dst + 2 * sub * U_::kTileBlk + l * sub * 64, p_sz[l], zb, bar, pol);
+      }
+    }
+    __syncwarp();
     #pragma unroll
     for (int l = 0; l < 2; ++l) {
-      bulk_load_hint(dst + l * sub * U_::kTileBlk, p_src[l], bytes, bar, pol);
-      if constexpr (PG) bulk_load_hint(dst + 2 * sub * U_::kTileBlk + l * sub * 64, p_sz[l], zb, bar, pol);
       p_src[l] += bytes;
       p_sz[l] += zb;
     }
@@ -167,9 +174,10 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
       mbar_init(wbar, kWarps);
     }
     fence_mbar_init();
-    point();
-    for (int i = 0; i < S; ++i) issue();   // the weights do not depend on the previous kernel
   }
+  __syncwarp();
+  point();
+  for (int i = 0; i < S; ++i) issue();   // the weights do not depend on the previous kernel
   // static too: the weak indices and the per-channel pairs
   for (int e = threadIdx.x; e < (a.nsl[0] + a.nsl[1]) * 16; e += kThreads) {
     const int l = e >= a.nsl[0] * 16, t = l ? e - a.nsl[0] * 16 : e;
@@ -379,11 +387,9 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
         }
       }
       __syncwarp();   // every lane has read the stage
-      if (lane == 0) {
-        --in_flight;
-        fence_proxy_async_smem();
-        issue();
-      }
+      --in_flight;
+      fence_proxy_async_smem();
+      issue();
       if (++st == S) { st = 0; phase ^= 1u; }
       left -= cnt;
       u += cnt;
