@@ -937,29 +937,57 @@ unsigned blocks_for(size_t n, int threads, unsigned most) {
   return (unsigned)std::max<size_t>(1, std::min<size_t>((n + threads - 1) / threads, most));
 }
 
-// Tokens of a tile.  A tile's time is set by forming the A operand up to about 128 tokens and by
-// the MMAs above, so one wide tile beats two narrower ones.
-int gated_tile_tokens(int M) { return M <= 64 ? 64 : M <= 128 ? 128 : M <= 192 ? 192 : 256; }
+// Measured times (us): a step of 128 codes, and of a tile what its neighbours do not hide (the
+// accumulator's way out).  Steps below 256 tokens are paced by forming the A operand, which the
+// tokens share; from there on by the MMAs.
+struct TileCost {
+  double step, tile;
+};
+TileCost fwd_cost(int BN) { return {BN == 64 ? 0.37 : BN == 128 ? 0.41 : BN == 192 ? 0.51 : 0.68, 0.016 * BN}; }
+TileCost ig_cost(int BN) { return {BN == 64 ? 0.44 : BN == 128 ? 0.54 : BN == 192 ? 0.65 : 0.81, 0.010 * BN}; }
 
 // The split of T tiles of `steps` steps over the SM pairs (see TileSplit): at least 4 steps a split, and
-// only where the saved time, in units of a step (about 0.3 us for 64 tokens to 0.65 us for 256),
-// exceeds the partials' way through L2 and the reduction's launch (about 4 us).
-TileSplit plan_split(long long T, int steps, int BN, int sms) {
+// only where the saved steps exceed the partials' way through L2 and the reduction's launch (about
+// 4 us).  `us`: the estimate of the whole product.
+TileSplit plan_split(long long T, int steps, int BN, TileCost c, int sms, double& us) {
   const int P = std::max(1, sms / 2);
   TileSplit s = {(int)T, (int)T, 1, steps};
+  us = (double)((T + P - 1) / P) * (steps * c.step + c.tile);
   const int rem = (int)(T % P);
   if (rem == 0) return s;
   int n = std::min(P / rem, steps / 4);
   if (n < 2) return s;
   const int per = (steps + n - 1) / n;
   n = (steps + per - 1) / per;
-  const double step_us = BN == 64 ? 0.3 : BN == 128 ? 0.4 : 0.65;
   const double cost_us = 4.0 + 4.0 * n * rem * BN * kBM * sizeof(float) / 5e6;
-  if ((steps - per) * step_us <= cost_us) return s;
+  if ((steps - per) * c.step <= cost_us) return s;
+  us -= (steps - per) * c.step - cost_us;
   s.whole = (int)(T - rem);
   s.splits = n;
   s.steps = per;
   return s;
+}
+
+// Tokens of a tile, for `rows` tiles across the other dimension: the width with the least estimate, a
+// narrower one only for 5% and 1 us less.  Wide tiles form an A operand for more tokens; narrower ones
+// leave fewer columns beyond M and fill the last wave better.  Measured, forward: 5461 x 2048 at 333
+// tokens, tiles of 128 / 192 / 256: 24.4 / 26.7 / 33.0 us; 11008 x 4096 at 256 tokens: 50.5 / 56.8 /
+// 44.0 us.  Over 120 products (six shapes, 64 to 1024 tokens, both directions) the choice is within
+// 0.4% of the best width on average and 11% at most.
+int pick_tile(int M, long long rows, int steps, int sms, TileCost (*cost)(int), TileSplit& split) {
+  int best = 0;
+  double best_us = 0;
+  for (int BN = 256; BN >= 64; BN -= 64) {
+    if (BN > 64 && M <= BN - 64) continue;   // (a narrower one holds them all)
+    double us;
+    const TileSplit s = plan_split(rows * ((M + BN - 1) / BN), steps, BN, cost(BN), sms, us);
+    if (!best || us < 0.95 * best_us - 1.0) {
+      best = BN;
+      best_us = us;
+      split = s;
+    }
+  }
+  return best;
 }
 size_t partial_bytes(const TileSplit& s, int BN) {
   return s.splits > 1 ? up256((size_t)s.splits * (s.tiles - s.whole) * 2 * BN * kBM * sizeof(float)) : 0;
@@ -987,9 +1015,8 @@ struct FwdPlan {
 };
 FwdPlan fwd_plan(const Layer& gate, const Layer& up, int M) {
   FwdPlan f;
-  f.BN = gated_tile_tokens(M);
   f.rts = (gate.N + 2 * kHalfRows - 1) / (2 * kHalfRows);
-  f.split = plan_split((long long)f.rts * ((M + f.BN - 1) / f.BN), gate.K / kStepCodes, f.BN, layer_sm_count(gate.device));
+  f.BN = pick_tile(M, f.rts, gate.K / kStepCodes, layer_sm_count(gate.device), fwd_cost, f.split);
   size_t at = 0;
   const Layer* L[2] = {&gate, &up};
   for (int l = 0; l < 2; ++l) {
@@ -1093,8 +1120,7 @@ struct IgPlan {
 IgPlan ig_plan(const Layer& gate, const Layer& up, int M) {
   IgPlan f;
   const int sms = layer_sm_count(gate.device);
-  f.BN = gated_tile_tokens(M);
-  f.split = plan_split((long long)((gate.K / kStepCodes + 1) / 2) * ((M + f.BN - 1) / f.BN), 2 * ((gate.N + 127) / 128), f.BN, sms);
+  f.BN = pick_tile(M, (gate.K / kStepCodes + 1) / 2, 2 * ((gate.N + 127) / 128), sms, ig_cost, f.split);
   f.ldy = (gate.N + 7) & ~7;
   size_t at = 0;
   for (int l = 0; l < 2; ++l) {
