@@ -645,69 +645,72 @@ owq_status_t owq_clip_create(const owq_grad_t* grads, int count, owq_stream_t st
   *out = nullptr;
   if (count < 0 || count > (1 << 20)) return OWQ_ERR_SHAPE;
   if (count > 0 && !grads) return OWQ_ERR_NULL;
-  struct Range { uintptr_t lo, hi; int tensor; bool write; };
+  struct Range { uintptr_t lo, hi; bool write; };
   std::vector<Range> ranges;
-  long long total = 0;
-  for (int i = 0; i < count; ++i) {
-    const owq_grad_t& t = grads[i];
-    if (t.dtype != OWQ_F32 && t.dtype != OWQ_F16 && t.dtype != OWQ_BF16) return OWQ_ERR_ARG;
-    if (t.n < 0 || t.n > (1LL << 40)) return OWQ_ERR_SHAPE;
-    if (t.n == 0) continue;
-    if (!t.grad || !t.out) return OWQ_ERR_NULL;
-    const uintptr_t size = t.dtype == OWQ_F32 ? 4 : 2, in = (uintptr_t)t.grad, o = (uintptr_t)t.out, bytes = size * (uintptr_t)t.n;
-    if (in % size || o % size) return OWQ_ERR_ALIGN;
-    ranges.push_back({in, in + bytes, i, o == in});
-    if (o != in) ranges.push_back({o, o + bytes, i, true});
-    total += (long long)bytes;
-  }
-  // a value that one tensor writes is in no other range (two reads of the same values may overlap)
-  std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
-  uintptr_t read_end = 0, write_end = 0;
-  for (const Range& r : ranges) {
-    if (r.lo < write_end || (r.write && r.lo < read_end)) return OWQ_ERR_ARG;
-    (r.write ? write_end : read_end) = std::max(r.write ? write_end : read_end, r.hi);
-  }
-  owq_status_t st = check_device();
-  if (st) return st;
-  Clip* c = new (std::nothrow) Clip();
-  if (!c) return OWQ_ERR_NOMEM;
-  cudaGetDevice(&c->device);
-  c->chunks = nullptr;
-  c->part = nullptr;
-  const int sms = layer_sm_count(c->device);
-  c->chunk_bytes = clip_chunk_bytes(total, sms);
-  c->status = device_status_ptr();
-  if (!c->status) { delete c; return OWQ_ERR_CUDA; }
   std::vector<ClipChunk> table;
-  for (int i = 0; i < count; ++i) {
-    const owq_grad_t& t = grads[i];
-    const long long size = t.dtype == OWQ_F32 ? 4 : 2;
-    const char* in = static_cast<const char*>(t.grad);
-    char* o = static_cast<char*>(t.out);
-    for (long long at = 0; at < t.n;) {   // chunks end where the input is 16-byte aligned
-      long long n = (c->chunk_bytes - (long long)((uintptr_t)(in + at * size) & 15)) / size;
-      n = std::min(n, t.n - at);
-      table.push_back({in + at * size, o + at * size, (int)n, t.dtype});
-      at += n;
-      if (table.size() > (size_t)1 << 30) { delete c; return OWQ_ERR_SHAPE; }
+  Clip* c = nullptr;
+  try {   // (the host tables; no exception leaves a C entry)
+    long long total = 0;
+    for (int i = 0; i < count; ++i) {
+      const owq_grad_t& t = grads[i];
+      if (t.dtype != OWQ_F32 && t.dtype != OWQ_F16 && t.dtype != OWQ_BF16) return OWQ_ERR_ARG;
+      if (t.n < 0 || t.n > (1LL << 38)) return OWQ_ERR_SHAPE;
+      if (t.n == 0) continue;
+      if (!t.grad || !t.out) return OWQ_ERR_NULL;
+      const uintptr_t size = t.dtype == OWQ_F32 ? 4 : 2, in = (uintptr_t)t.grad, o = (uintptr_t)t.out, bytes = size * (uintptr_t)t.n;
+      if (in % size || o % size) return OWQ_ERR_ALIGN;
+      ranges.push_back({in, in + bytes, o == in});
+      if (o != in) ranges.push_back({o, o + bytes, true});
+      total += (long long)bytes;
+      if (total > (1LL << 40)) return OWQ_ERR_SHAPE;
     }
-  }
-  c->n_chunks = (int)table.size();
-  c->grid = std::max(1, std::min(sms, c->n_chunks));
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMalloc(&c->chunks, std::max<size_t>(1, table.size()) * sizeof(ClipChunk));
-  if (e == cudaSuccess) e = cudaMalloc(&c->part, (c->grid + 1) * sizeof(double));
-  if (e == cudaSuccess) {
-    c->arrived = reinterpret_cast<unsigned long long*>(c->part + c->grid);
-    e = cudaMemsetAsync(c->part, 0, (c->grid + 1) * sizeof(double), s);
-  }
-  if (e == cudaSuccess && c->n_chunks > 0)
-    e = cudaMemcpyAsync(c->chunks, table.data(), table.size() * sizeof(ClipChunk), cudaMemcpyHostToDevice, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);   // the host table must outlive its copy
-  if (e != cudaSuccess) { release_clip(c); return cuda_status(e); }
-  {
+    // a value that one tensor writes is in no other range (two reads of the same values may overlap)
+    std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    uintptr_t read_end = 0, write_end = 0;
+    for (const Range& r : ranges) {
+      if (r.lo < write_end || (r.write && r.lo < read_end)) return OWQ_ERR_ARG;
+      (r.write ? write_end : read_end) = std::max(r.write ? write_end : read_end, r.hi);
+    }
+    owq_status_t st = check_device();
+    if (st) return st;
+    c = new Clip();
+    cudaGetDevice(&c->device);
+    c->chunks = nullptr;
+    c->part = nullptr;
+    const int sms = layer_sm_count(c->device);
+    c->chunk_bytes = clip_chunk_bytes(total, sms);
+    c->status = device_status_ptr();
+    if (!c->status) { delete c; return OWQ_ERR_CUDA; }
+    for (int i = 0; i < count; ++i) {
+      const owq_grad_t& t = grads[i];
+      const long long size = t.dtype == OWQ_F32 ? 4 : 2;
+      const char* in = static_cast<const char*>(t.grad);
+      char* o = static_cast<char*>(t.out);
+      for (long long at = 0; at < t.n;) {   // chunks end where the input is 16-byte aligned
+        long long n = (c->chunk_bytes - (long long)((uintptr_t)(in + at * size) & 15)) / size;
+        n = std::min(n, t.n - at);
+        table.push_back({in + at * size, o + at * size, (int)n, t.dtype});
+        at += n;
+      }
+    }
+    c->n_chunks = (int)table.size();
+    c->grid = std::max(1, std::min(sms, c->n_chunks));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMalloc(&c->chunks, std::max<size_t>(1, table.size()) * sizeof(ClipChunk));
+    if (e == cudaSuccess) e = cudaMalloc(&c->part, (c->grid + 1) * sizeof(double));
+    if (e == cudaSuccess) {
+      c->arrived = reinterpret_cast<unsigned long long*>(c->part + c->grid);
+      e = cudaMemsetAsync(c->part, 0, (c->grid + 1) * sizeof(double), s);
+    }
+    if (e == cudaSuccess && c->n_chunks > 0)
+      e = cudaMemcpyAsync(c->chunks, table.data(), table.size() * sizeof(ClipChunk), cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);   // the host table must outlive its copy
+    if (e != cudaSuccess) { release_clip(c); return cuda_status(e); }
     std::lock_guard<std::mutex> g(g_mu);
     clip_registry().insert(c);
+  } catch (const std::bad_alloc&) {
+    if (c) release_clip(c);
+    return OWQ_ERR_NOMEM;
   }
   *out = reinterpret_cast<owq_clip_t>(c);
   return OWQ_OK;
