@@ -48,10 +48,10 @@ typedef int owq_status_t;
 #define OWQ_ERR_ALIGN     6   /* a device pointer is not 16-byte aligned                      */
 #define OWQ_ERR_CUDA      7   /* a CUDA runtime call or a launch failed                       */
 #define OWQ_ERR_TIMEOUT   8   /* a bounded device-side wait gave up (see owq_device_status)    */
-#define OWQ_ERR_NOMEM     9   /* a device or host allocation failed                           */
+#define OWQ_ERR_NOMEM     9   /* an allocation failed, or a given workspace is too small       */
 #define OWQ_ERR_HANDLE    10  /* the layer handle is NULL or not one this library made         */
 #define OWQ_ERR_DEVICE    11  /* no CUDA device, or the device is not sm_100                   */
-#define OWQ_ERR_ARG       12  /* an argument outside its documented set (owq_debug_inject)      */
+#define OWQ_ERR_ARG       12  /* an argument outside its documented set (an activation, a type, ranges that overlap) */
 #define OWQ_ERR_BOUNDS    13  /* debug-bounds build: a device index check failed (owq_device_status) */
 
 /* Failures owq_debug_inject can arm. */
@@ -386,13 +386,15 @@ owq_status_t owq_input_grad(owq_layer_t layer, const uint16_t* dy, uint16_t* dx,
  * (OWQ_ERR_DEVICE); their weak columns may differ, and they may be the same handle.  Nothing is
  * kept in the handles: calls on any streams may overlap and may be captured, as long as their
  * outputs and workspaces do not.  x, dh and so on are row-major and contiguous; outputs are
- * fully overwritten and must not overlap inputs.  Waits are bounded (OWQ_ERR_TIMEOUT through
+ * fully overwritten and must overlap neither inputs nor one another.  A value that is not finite
+ * leaves its own token's outputs not finite or undefined, no other token's.  Waits are bounded (OWQ_ERR_TIMEOUT through
  * owq_device_status; outputs are then undefined).  Repeated calls give identical bits.
  */
 
 /*
- * owq_gated_gemv -- h for 1 <= M <= 16 tokens in one launch, bound by reading the packed
- * weights once.  In: x fp16 M x K.  Out: h fp16 M x N.  No workspace.
+ * owq_gated_gemv -- h for 1 <= M <= 16 tokens, bound by reading the packed weights once.  In: x
+ * fp16 M x K.  Out: h fp16 M x N.  No workspace.  One launch (several over parts of N where the
+ * sums of a launch's tiles would crowd out the weights' rings: very many rows at 16 tokens).
  */
 owq_status_t owq_gated_gemv(owq_layer_t gate, owq_layer_t up, int act, const uint16_t* x,
                             uint16_t* h, int M, owq_stream_t stream);
@@ -460,8 +462,8 @@ owq_status_t owq_clip_create(const owq_grad_t* grads, int count, owq_stream_t st
  * fp64) and out = grad * min(1, *norm finite ? max_norm / (*norm + 1e-6) : 1) for every tensor,
  * multiplied in fp32 and rounded once.  A norm that is not finite clips nothing: the caller
  * reads it and skips the step.  In place and unclipped, nothing is written.  max_norm >= 0
- * (infinity: the norm alone; OWQ_ERR_ARG for negative or NaN).  One cooperative launch, allowed
- * in a capture.  Calls on one handle must be ordered (they share its partial sums); the handle
+ * (infinity: the norm alone, in place nothing is written; OWQ_ERR_ARG for negative or NaN).  `norm`
+ * (16-byte aligned) lies in none of the tensors.  One cooperative launch, allowed in a capture.  Calls on one handle must be ordered (they share its partial sums); the handle
  * belongs to the device it was created on (OWQ_ERR_DEVICE).  A bounded wait that gives up
  * leaves the outputs undefined.  Repeated calls give identical bits.
  */
@@ -509,7 +511,7 @@ owq_status_t owq_device_status(void);
  *                           are split across CTAs are published under a tag no reader accepts,
  *                           so each cross-CTA wait runs out and its tile is not written (a
  *                           layer whose tiles all stay inside one CTA has no such wait);
- *   OWQ_INJECT_GEMM_ARRIVE  next owq_gemm: one dequantisation thread of every CTA skips its
+ *   OWQ_INJECT_GEMM_ARRIVE  next owq_gemm or owq_gated_gemm: one dequantisation thread of every CTA skips its
  *                           arrival for its first K step, so the MMA issuer's wait runs out,
  *                           then the producer's and the dequantisation threads' waits.
  * wait_cycles (>= 1) bounds every device wait of that call, in SM clock cycles (otherwise the

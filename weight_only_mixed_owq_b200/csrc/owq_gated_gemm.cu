@@ -11,7 +11,11 @@
 // type that activations and gradients have at every layer boundary of this library), dx once.
 //
 // Bound: the tensor cores from about 200 tokens (4 M N K flops forward, 8 M N K backward), the
-// packed weights' bytes below.
+// packed weights' bytes below.  Measured (GPU time): 13824 x 5120, 3-bit, 2048 tokens forward 395 us
+// (1.47 PFLOP/s), backward 845 us (1.37); 11008 x 4096, 4-bit, 64 tokens forward 28.2 us, 256 tokens
+// backward 96 us.  Below 256 tokens a step (128 codes of 256 MMA rows by the tile's tokens) is paced
+// by forming the A operand: 0.35 / 0.39 / 0.50 us at 64 / 128 / 192 tokens (3-bit), 0.67 us at 256,
+// where the MMAs alone want 0.53 us at the full clock.
 #include <algorithm>
 #include <type_traits>
 
@@ -40,8 +44,8 @@ struct Stage {
   static constexpr int kP = kBM * 16 * BITS;
   static constexpr int kSZ = kBM * 4;
   static constexpr int kBytes = ((kX + kP + kSZ) + 1023) & ~1023;
-  // stages: what fits, at most 12 (the ring covers the latency of the loads: a step takes 0.3 to
-  // 0.6 us, a load from HBM through both rings to the MMA's end about 3 us)
+  // stages: what fits, at most 12 (the ring covers the latency of the loads: a step takes 0.35 to
+  // 0.7 us, a load from HBM through both rings to the MMA's end about 3 us)
   static constexpr int kFit = (232448 - 2048) / kBytes;
   static constexpr int kS = kFit < 12 ? kFit : 12;
 };
@@ -515,7 +519,7 @@ __global__ void k_gated_reduce(const __grid_constant__ GatedGemmParams p, int BN
 // rows packed per 32-bit column.  That is four instructions a pair beside the unpack, and shared
 // memory is read only for the packed words (forming the operand column by column took two 64-bit
 // shared loads and six instructions per pair of rows: 131 KB of shared reads a step, as long as
-// the MMAs).
+// the MMAs).  A step takes 0.45 / 0.53 / 0.64 / 0.80 us at 64 / 128 / 192 / 256 tokens.
 // The weak columns' codes give exactly 0; their products with the fp16 weak blocks come from
 // k_gated_igw, running beside this kernel, and are added in fp32 in the epilogue of a tile's first
 // split, so that a column that is weak in one layer and packed in the other is rounded once.
@@ -833,7 +837,10 @@ __global__ void k_gated_ig_reduce(const __grid_constant__ GatedIgParams p, int B
 // The weak columns' products of both layers, wk[l][row split][slot][m] = sum_i dy_l[m][i]
 // w_weak_l[i][slot] (mma.sync m16n8k16: rows = tokens, K = weight rows, columns = slots).  A CTA of
 // 4 warps computes 64 tokens x CT slots of one layer over one split of the rows, 64 rows at a time
-// through a 4-stage cp.async ring.  Bound by reading the gradients, once per CT slots.
+// through a 4-stage cp.async ring.  Bound by reading the gradients, once per CT slots: 13824 rows,
+// 2048 tokens, 40 slots of each layer 36.8 us (113 MB, 3.1 TB/s; 46 us with 64-byte pieces and five
+// splits), 11008 rows, 256 tokens 7.1 us.  (Weak columns put into the A operand instead, loaded over
+// their dequantised registers, made every step longer: 866 -> 937 us at 2048 tokens.)
 constexpr int kIwTok = 64, kIwRows = 64, kIwThreads = 128, kIwStages = 4, kIwMaxSplits = 16;
 constexpr int kIwDyLd = kIwRows + 8;   // padded row stride (halves)
 

@@ -1,6 +1,7 @@
 // Thin inline-PTX wrappers for the sm_100a features the library's kernels use: mbarriers, bulk
-// and TMA tile loads (no cluster multicast anywhere in this library), thread-block clusters and
-// distributed shared memory, tcgen05 MMA / TMEM.
+// and TMA tile loads (no load with cluster multicast anywhere in this library; an MMA commit may
+// arrive on the barriers of both CTAs of a pair), thread-block clusters and distributed shared
+// memory, tcgen05 MMA / TMEM.
 #pragma once
 #include <cstdint>
 
