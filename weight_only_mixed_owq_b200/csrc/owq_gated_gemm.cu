@@ -382,7 +382,6 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
       for (; i < stop && ok; i += kGR) {
         // weak step: slab jh covers columns c0 .. c0 + 8 U - 1 of layer wl's part of the step
         const int g = g0 + i, wl = (8 * U * jh) / 64, c0 = (i - nD) * 64 + (8 * U * jh) % 64;
-        if (!(ok = ready(g))) break;
         const uint4* src = reinterpret_cast<const uint4*>(p.w_weak[lay] + (size_t)row * p.k_ld[lay] + c0);
         uint32_t d[U / 4][16];
         #pragma unroll
@@ -391,6 +390,7 @@ k_gated_gemm(const __grid_constant__ GatedMaps maps, const __grid_constant__ Gat
           d[v >> 2][4 * (v & 3)] = q.x; d[v >> 2][4 * (v & 3) + 1] = q.y;
           d[v >> 2][4 * (v & 3) + 2] = q.z; d[v >> 2][4 * (v & 3) + 3] = q.w;
         }
+        if (!(ok = ready(g))) break;   // (the weak block is static: its loads are under way meanwhile)
         put(g, d);
       }
       if (!ok) break;
