@@ -445,6 +445,7 @@ class OwqGated:
         self.gate, self.up, self.act = gate, up, self.ACTS[act]
         self.N, self.K = gate.N, gate.K
         self._torch, self._half = torch, torch.float16
+        self._ws_size = (0, 0)   # (M, bytes) of the last workspace
 
     def _rows(self, t, name: str, width: int) -> int:
         if t.dim() != 2:
@@ -454,15 +455,22 @@ class OwqGated:
             _check_tensor(t, name, (M, width), self._half)
         return M
 
+    def _with(self, t, name: str, M: int, width: int, like) -> None:
+        if t.shape != (M, width) or t.dtype != self._half or t.device != like.device or not t.is_contiguous():
+            _check_tensor(t, name, (M, width), self._half, like.device)
+
     def _out(self, t, name: str, M: int, width: int, like):
         if t is None:
             return like.new_empty((M, width))
-        _check_tensor(t, name, (M, width), self._half, like.device)
+        self._with(t, name, M, width, like)
         return t
 
     def _workspace(self, M: int, like):
-        st, n = owq_gated_workspace(self.gate.handle, self.up.handle, M)
-        _check(st, "owq_gated_workspace")
+        last, n = self._ws_size
+        if last != M:
+            st, n = owq_gated_workspace(self.gate.handle, self.up.handle, M)
+            _check(st, "owq_gated_workspace")
+            self._ws_size = (M, n)
         return like.new_empty((n,), dtype=self._torch.uint8), n
 
     def gemv(self, x, h=None, stream=None):
@@ -503,13 +511,13 @@ class OwqGated:
     def grad(self, x, dh, dgate=None, dup=None, stream=None):
         """(dgate, dup): the gradients of x Wg^T and x Wu^T, recomputed from x."""
         M = self._rows(x, "x", self.K)
-        _check_tensor(dh, "dh", (M, self.N), self._half, x.device)
+        self._with(dh, "dh", M, self.N, x)
         return _run_on(self._torch, x.device, stream, lambda s: self._grad(x, dh, dgate, dup, M, *self._workspace(M, x), s))
 
     def input_grad(self, dgate, dup, dx=None, stream=None):
         """dx = dgate Wg + dup Wu."""
         M = self._rows(dgate, "dgate", self.N)
-        _check_tensor(dup, "dup", (M, self.N), self._half, dgate.device)
+        self._with(dup, "dup", M, self.N, dgate)
         return _run_on(self._torch, dgate.device, stream,
                        lambda s: self._input_grad(dgate, dup, dx, M, *self._workspace(M, dgate), s))
 
@@ -517,7 +525,7 @@ class OwqGated:
         """(dx, dgate, dup) from the gradient dh of h.  The weak blocks' gradients follow with
         gate.weak_grad(x, dgate) and up.weak_grad(x, dup)."""
         M = self._rows(x, "x", self.K)
-        _check_tensor(dh, "dh", (M, self.N), self._half, x.device)
+        self._with(dh, "dh", M, self.N, x)
 
         def go(s):
             ws, n = self._workspace(M, x)
