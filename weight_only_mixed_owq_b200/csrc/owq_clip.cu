@@ -11,8 +11,8 @@
 // waits for the others' (bounded).  The second pass walks the chunks backwards: the last ones are
 // still in the ring, the ones before them in L2, where the streaming stores leave them until they
 // are read.
-// Measured: 202 MB of fp32 in 224 tensors 103 us; of the second pass's 202 MB about 60 MB come
-// from the ring and L2 (344 MB read from memory), 546 MB through memory in all: 5.3 TB/s.
+// Measured: 202 MB of fp32 in 224 tensors 97 us; 333 MB read, so that 71 MB of the second pass's
+// input came from the ring and L2: 535 MB through memory, 5.5 TB/s.
 // Squares are added in fp64, eight values' worth at a time: those are summed in fp32 (2^-24 each,
 // averaging out) where that neither overflows nor loses small values, else one by one in fp64 (a
 // conversion per value would take as long as the memory).  All sums run in a fixed order: repeated
@@ -30,11 +30,16 @@ using namespace sm100;
 constexpr int kWarps = 16, kThreads = kWarps * 32;   // and the producer warp
 constexpr int kChunkBytes = 32 * 1024;               // most bytes of a chunk
 constexpr int kRingBytes = 6 * kChunkBytes, kMaxSlots = 16;
+// What the first pass leaves in L2 (126 MB) for the second; the rest is loaded evict-first.  202 MB
+// of fp32 with 0 / 40 / 60 / 80 / 100 / 120 / 140 MB: 102.5 / 101.5 / 100.9 / 97.1 / 97.3 / 97.8 / 98.9 us,
+// without any hint 101.8 (the L2's evict-last priority for what is left gave the same).
+constexpr int kKeepBytes = 90 << 20;
 
 struct ClipArgs {
   const ClipChunk* chunks;
   int n_chunks;
   int slot_bytes, slots;
+  int keep;                      // a CTA's last chunks that the second pass may find in L2
   double* part;                  // [gridDim.x] partial sums
   unsigned long long* arrived;   // CTAs that have published, over all calls
   float max_norm;
@@ -186,13 +191,18 @@ __global__ void __launch_bounds__(kThreads + 32, 1) k_clip(const __grid_constant
     // one lane copies; the warp fetches the table entries 32 at a time
     bool ok = true;
     ClipChunk mineq = {};
-    auto load = [&](int i, const ClipChunk& c) {
+    uint64_t first;   // evict first: what the second pass will not find in L2 anyway, or has read
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
+    auto load = [&](int i, const ClipChunk& c, bool keep) {
       const int s = i % S, size = c.dtype == OWQ_F32 ? 4 : 2;
       const int head = min(c.n, (int)((16 - (reinterpret_cast<uintptr_t>(c.in) & 15)) & 15) / size);
       const uint32_t bytes = (uint32_t)((c.n - head) * size) & ~15u;
       s_chunk[s] = c;
       mbar_arrive_expect_tx(&full[s], bytes);
-      if (bytes) bulk_load(ring + (size_t)s * a.slot_bytes, static_cast<const char*>(c.in) + head * size, bytes, &full[s]);
+      if (bytes == 0) return;
+      const char* from = static_cast<const char*>(c.in) + head * size;
+      if (keep) bulk_load(ring + (size_t)s * a.slot_bytes, from, bytes, &full[s]);
+      else bulk_load_hint(ring + (size_t)s * a.slot_bytes, from, bytes, &full[s], first);
     };
     auto entry = [&](int at) {   // of the 32 this warp holds
       ClipChunk c;
@@ -206,7 +216,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) k_clip(const __grid_constant
       if (i % 32 == 0 && i + lane < mine) mineq = a.chunks[b + (size_t)(i + lane) * G];
       const ClipChunk c = entry(i % 32);
       if (i >= S) ok = __all_sync(0xffffffffu, mbar_wait(&empty[i % S], (uint32_t)(i / S - 1) & 1, a.status, a.wait_limit));
-      if (ok && lane == 0) load(i, c);
+      if (ok && lane == 0) load(i, c, i >= mine - a.keep);
       __syncwarp();
     }
     // Every slot's first-pass uses are consumed before the second pass waits on the slots' barriers: a
@@ -217,7 +227,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) k_clip(const __grid_constant
       const ClipChunk c = entry(k % 32);
       // the second pass's use of the slot by chunk i + S is over: its consumption follows the first pass's
       ok = __all_sync(0xffffffffu, mbar_wait(&empty[i % S], (uint32_t)uses.second(i) & 1, a.status, a.wait_limit));
-      if (ok && lane == 0) load(i, c);
+      if (ok && lane == 0) load(i, c, false);
       __syncwarp();
     }
     // never leave with copies in flight: the last copy into every slot
@@ -306,6 +316,7 @@ cudaError_t launch_clip(const Clip& c, float max_norm, float* norm, long long wa
   a.status = c.status;
   a.wait_limit = wait_limit;
   const int per = (c.n_chunks + c.grid - 1) / c.grid;
+  a.keep = kKeepBytes / (c.chunk_bytes * c.grid);
   a.slots = std::max(1, std::min({per, kRingBytes / c.chunk_bytes, kMaxSlots}));
   const int smem = a.slots * c.chunk_bytes;
   static std::atomic<unsigned long long> allowed{0};
