@@ -33,7 +33,7 @@
 // distributed shared memory: repeated calls give identical bits.
 //
 // Measured (a graph of calls over three copies of the weights, GPU time per call): 11008 x 4096,
-// 4-bit, one token 14.0 us (49.4 MB, 3.5 TB/s; a further tile of 16 x 4096 per CTA costs 1.95 us,
+// 4-bit, one token 13.9 us (49.4 MB, 3.5 TB/s; a further tile of 16 x 4096 per CTA costs 1.95 us,
 // 5.4 TB/s, the rest about 5.7 us a launch); 13824 x 5120, 3-bit, 16 tokens 28.5 us (two token tiles
 // through the products: issue-bound, 2.2 warp instructions a cycle per SM).
 #include "owq_act.cuh"
