@@ -150,3 +150,41 @@ def test_a_fine_tuning_step(owq, M):
         got = [c.clone() for c in (*captured, *s.clipped)]
         assert all(torch.equal(p, q) for p, q in zip(got, (*s(0.01), *s.clipped)))
     assert owq.owq_device_status() == 0
+
+
+def test_offsets_past_32_bits(owq):
+    """65536 tokens of 32805 outputs: more than 2^31 values in h and in every gradient (odd rows, so the
+    gradients are padded too); the first and last tokens against 64 bits."""
+    N, K, M = 32805, 128, 65536
+    (gate, Wg), (up, Wu) = (layer(owq, N, K, 4, 128, k, 70 + k) for k in (2, 0))
+    b = owq.OwqGated(gate, up)
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    x = torch.randn(M, K, generator=gen, device=DEV, dtype=torch.float16)
+    at = torch.tensor([0, 1, M // 2, M - 2, M - 1], device=DEV)
+    h = b.gemm(x)
+    want, bound = ref.forward(x[at], Wg, Wu, "silu")
+    ref.check(h[at], want, bound, "h")
+    dh = h.mul_(0.01)
+    dx, g, u = b.backward(x, dh)
+    dg, bg, du, bu = ref.backward(x[at], dh[at], Wg, Wu, "silu")
+    ref.check(g[at], dg, bg, "dgate")
+    ref.check(u[at], du, bu, "dup")
+    want, bound = ref.input_grad(g[at], u[at], Wg, Wu)
+    ref.check(dx[at], want, bound, "dx")
+    assert owq.owq_device_status() == 0
+
+
+def test_clipping_a_tensor_past_32_bits(owq):
+    """2^31 + 77 values of one, two of which are far larger, at the ends; in place."""
+    n = 2 ** 31 + 77
+    g = torch.ones(n, dtype=torch.bfloat16, device=DEV)
+    g[0], g[-1] = 30000.0, -20032.0
+    assert float(g[0]) == 29952.0
+    norm64 = math.sqrt(n - 2 + 29952.0 ** 2 + float(g[-1]) ** 2)
+    last = float(g[-1])
+    norm = float(owq.clip_grads([g], norm64 / 4))
+    assert abs(norm - norm64) <= 2.0 ** -22 * norm64
+    f = 0.25 * norm64 / (norm64 + 1e-6)
+    for i, v in ((0, 29952.0), (1, 1.0), (2 ** 31 - 1, 1.0), (2 ** 31 + 5, 1.0), (n - 1, last)):
+        assert abs(float(g[i]) - v * f) <= abs(v * f) * (2.0 ** -8 + 2.0 ** -21)
+    assert bool((g[1:-1].view(torch.int16) == g[1].view(torch.int16)).all())
