@@ -400,8 +400,8 @@ owq_status_t owq_gated_gemv(owq_layer_t gate, owq_layer_t up, int act, const uin
                             uint16_t* h, int M, owq_stream_t stream);
 
 /*
- * owq_gated_workspace -- bytes of workspace that owq_gated_gemm, owq_gated_grad and
- * owq_gated_input_grad each need at most for M tokens (host call; 1 <= M <= 65536).  The
+ * owq_gated_workspace -- bytes of workspace that owq_gated_gemm, owq_gated_grad,
+ * owq_gated_input_grad and owq_gated_backward each need at most for M tokens (host call; 1 <= M <= 65536).  The
  * workspace needs no initialisation and carries nothing from one call to the next.
  */
 owq_status_t owq_gated_workspace(owq_layer_t gate, owq_layer_t up, int M, size_t* bytes);
@@ -433,6 +433,15 @@ owq_status_t owq_gated_grad(owq_layer_t gate, owq_layer_t up, int act, const uin
 owq_status_t owq_gated_input_grad(owq_layer_t gate, owq_layer_t up, const uint16_t* dgate,
                                   const uint16_t* dup, uint16_t* dx, int M, void* ws,
                                   size_t ws_bytes, owq_stream_t stream);
+
+/*
+ * owq_gated_backward -- the whole backward pass: owq_gated_grad, then dx (M x K).  Up to 32 tokens dx
+ * is formed from dgate and dup before their rounding (22 bits of them), so that it carries its own
+ * rounding only; beyond, it is owq_gated_input_grad of the returned dgate and dup, bit for bit.
+ */
+owq_status_t owq_gated_backward(owq_layer_t gate, owq_layer_t up, int act, const uint16_t* x,
+                                const uint16_t* dh, uint16_t* dgate, uint16_t* dup, uint16_t* dx,
+                                int M, void* ws, size_t ws_bytes, owq_stream_t stream);
 
 /* Gradient tensors of owq_clip_create: n contiguous values of `dtype` (device pointers, aligned
  * to the value's size; out may equal grad: in place; both may be NULL when n == 0). */

@@ -21,6 +21,7 @@ def test_gated_calls_want_live_handles(owq):
         assert owq.owq_gated_gemv(gate, up, 0, FAKE, FAKE, 1) == 10
         assert owq.owq_gated_gemm(gate, up, 0, FAKE, FAKE, 64, FAKE, 1 << 20) == 10
         assert owq.owq_gated_grad(gate, up, 0, FAKE, FAKE, FAKE, FAKE, 64, FAKE, 1 << 20) == 10
+        assert owq.owq_gated_backward(gate, up, 0, FAKE, FAKE, FAKE, FAKE, FAKE, 64, FAKE, 1 << 20) == 10
         assert owq.owq_gated_input_grad(gate, up, FAKE, FAKE, FAKE, 64, FAKE, 1 << 20) == 10
         assert owq.owq_gated_workspace(gate, up, 64)[0] == 10
 

@@ -87,6 +87,60 @@ def test_a_token_that_is_not_finite_stays_alone(owq, M):
     assert owq.owq_device_status() == 0
 
 
+def input_grad(x, dh, dg, du, Wg, Wu, act):
+    """dx of a whole backward pass and its bound: above 32 tokens from the returned dgate and dup, up to 32
+    from the unrounded ones, of which two fp16 halves keep 2^-22 (2^-25 below fp16's normal range)."""
+    if x.shape[0] > 32:
+        return ref.input_grad(dg, du, Wg, Wu)
+    g, bg, u, bu = ref.backward(x, dh, Wg, Wu, act)
+    want, bound = ref.input_grad(g, u, Wg, Wu)
+    for v, b, W in ((g, bg, Wg), (u, bu, Wu)):
+        fp32 = (b - ref.half_spacing(v) * 1.001).clamp(min=0)   # what is not the returned value's rounding
+        bound = bound + (fp32 + v.abs() * 2.0 ** -22 + 2.0 ** -25) @ W.abs()
+    return want, bound
+
+
+# few tokens: one of them, all columns weak, odd row lengths (their pads), tiles without and with a K split
+FEW = [(600, 4736, 4, 128, 40, 70), (4805, 384, 3, 384, 7, 0), (37, 256, 4, 128, 256, 3), (130, 19456, 3, 128, 0, 19), (8, 128, 4, 128, 0, 0)]
+
+
+@pytest.mark.parametrize("M", [1, 7, 8, 32, 33])
+@pytest.mark.parametrize("shape", FEW, ids=str)
+def test_backward_of_few_tokens(owq, shape, M):
+    """dx against the unrounded formula, and into the next buffers no value; above 32 tokens, bit for bit
+    the separate calls."""
+    (gate, Wg), (up, Wu) = pair(owq, *shape)
+    act = ("silu", "gelu", "gelu_tanh")[M % 3]
+    b = owq.OwqGated(gate, up, act)
+    N, K = shape[:2]
+    x, dh = rand(M, M, K), rand(M + 1, M, N, scale=0.1)
+    guard = torch.full((M + 64, K), 3.0, dtype=torch.float16, device=DEV)
+    dx, g, u = b.backward(x, dh, dx=guard[:M])
+    assert bool((guard[M:] == 3.0).all())
+    sg, su = b.grad(x, dh)
+    assert torch.equal(g, sg) and torch.equal(u, su)
+    want, bound = input_grad(x, dh, g, u, Wg, Wu, act)
+    ref.check(dx, want, bound, "dx")
+    if M > 32:
+        assert torch.equal(dx, b.input_grad(g, u))
+    again = b.backward(x, dh)
+    assert all(torch.equal(p, q) for p, q in zip((dx, g, u), again))
+    assert owq.owq_device_status() == 0
+
+
+def test_backward_halves_are_finite_where_the_gradient_overflows(owq):
+    """A dgate past fp16's range is an infinity in its own token and column; dx is not finite there, not
+    elsewhere."""
+    (gate, _), (up, _) = pair(owq, 37, 256, 4, 128, 256, 3)
+    b = owq.OwqGated(gate, up)
+    x, dh = rand(1, 9, 256, scale=100.0), rand(2, 9, 37, scale=1.0)
+    dh[4] = 60000.0
+    dx, g, u = b.backward(x, dh)
+    keep = torch.arange(9, device=DEV) != 4
+    assert not bool(torch.isfinite(g[4]).all()) and not bool(torch.isfinite(dx[4]).any())
+    assert bool(torch.isfinite(dx[keep]).all())
+
+
 def weak_grad64(x, dy, idx):
     """dy^T x at the weak columns, and a bound of its fp32 sums."""
     a, d = x.double()[:, idx.long()], dy.double()
@@ -128,7 +182,7 @@ def test_a_fine_tuning_step(owq, M):
     want, bg, wantu, bu = ref.backward(s.x, dh, s.Wg, s.Wu, "silu")
     ref.check(dg, want, bg, "dgate")
     ref.check(du, wantu, bu, "dup")
-    want, bound = ref.input_grad(dg, du, s.Wg, s.Wu)
+    want, bound = input_grad(s.x, dh, dg, du, s.Wg, s.Wu, "silu")
     ref.check(dx, want, bound, "dx")
     for l, a, d, dw, what in ((s.gate, s.x, dg, s.dw[0], "gate"), (s.up, s.x, du, s.dw[1], "up"), (s.down, h, dy, s.dw[2], "down")):
         want, bound = weak_grad64(a, d, l.weak)

@@ -50,6 +50,7 @@ PROTOTYPES = [
     ("owq_gated_workspace", _I, [_P, _P, _I, _SZ]),
     ("owq_gated_gemm", _I, [_P, _P, _I, _P, _P, _I, _P, ctypes.c_size_t, _P]),
     ("owq_gated_grad", _I, [_P, _P, _I, _P, _P, _P, _P, _I, _P, ctypes.c_size_t, _P]),
+    ("owq_gated_backward", _I, [_P, _P, _I, _P, _P, _P, _P, _P, _I, _P, ctypes.c_size_t, _P]),
     ("owq_gated_input_grad", _I, [_P, _P, _P, _P, _P, _I, _P, ctypes.c_size_t, _P]),
     ("owq_clip_create", _I, [_P, _I, _P, ctypes.POINTER(_P)]),
     ("owq_clip_grads", _I, [_P, ctypes.c_float, _P, _P]),
@@ -223,6 +224,11 @@ def owq_gated_grad(gate, up, act, x, dh, dgate, dup, M, ws, ws_bytes, stream=Non
 
 def owq_gated_input_grad(gate, up, dgate, dup, dx, M, ws, ws_bytes, stream=None) -> int:
     return LIB.owq_gated_input_grad(gate, up, _ptr(dgate), _ptr(dup), _ptr(dx), M, _ptr(ws), ws_bytes, _stream(stream))
+
+
+def owq_gated_backward(gate, up, act, x, dh, dgate, dup, dx, M, ws, ws_bytes, stream=None) -> int:
+    return LIB.owq_gated_backward(gate, up, act, _ptr(x), _ptr(dh), _ptr(dgate), _ptr(dup), _ptr(dx), M, _ptr(ws), ws_bytes,
+                                  _stream(stream))
 
 
 class OwqGrad(ctypes.Structure):
@@ -522,15 +528,18 @@ class OwqGated:
                        lambda s: self._input_grad(dgate, dup, dx, M, *self._workspace(M, dgate), s))
 
     def backward(self, x, dh, dx=None, dgate=None, dup=None, stream=None):
-        """(dx, dgate, dup) from the gradient dh of h.  The weak blocks' gradients follow with
+        """(dx, dgate, dup) from the gradient dh of h (up to 32 tokens dx comes from dgate and dup
+        before their rounding, beyond it is input_grad(dgate, dup)).  The weak blocks' gradients follow with
         gate.weak_grad(x, dgate) and up.weak_grad(x, dup)."""
         M = self._rows(x, "x", self.K)
         self._with(dh, "dh", M, self.N, x)
 
         def go(s):
             ws, n = self._workspace(M, x)
-            g, u = self._grad(x, dh, dgate, dup, M, ws, n, s)
-            return self._input_grad(g, u, dx, M, ws, n, s), g, u
+            g, u, d = self._out(dgate, "dgate", M, self.N, x), self._out(dup, "dup", M, self.N, x), self._out(dx, "dx", M, self.K, x)
+            _check(LIB.owq_gated_backward(self.gate.handle, self.up.handle, self.act, x.data_ptr(), dh.data_ptr(), g.data_ptr(),
+                                          u.data_ptr(), d.data_ptr(), M, ws.data_ptr(), n, s), "owq_gated_backward")
+            return d, g, u
         return _run_on(self._torch, x.device, stream, go)
 
 

@@ -591,7 +591,7 @@ owq_status_t owq_gated_workspace(owq_layer_t gate, owq_layer_t up, int M, size_t
   if (st) return st;
   if (!bytes) return OWQ_ERR_NULL;
   if (M < 1 || M > 65536) return OWQ_ERR_SHAPE;
-  *bytes = std::max<size_t>(256, std::max(gated_gemm_ws_bytes(*g, *u, M), gated_input_grad_ws_bytes(*g, *u, M)));
+  *bytes = std::max<size_t>(256, std::max(gated_backward_ws_bytes(*g, *u, M), gated_input_grad_ws_bytes(*g, *u, M)));
   return OWQ_OK;
 }
 
@@ -638,6 +638,21 @@ owq_status_t owq_gated_input_grad(owq_layer_t gate, owq_layer_t up, const uint16
   return gated_input_grad_sm100(*g, *u, reinterpret_cast<const __half*>(dgate), reinterpret_cast<const __half*>(dup),
                                 reinterpret_cast<__half*>(dx), M, ws, ws_bytes, kDefaultWaitLimit,
                                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+owq_status_t owq_gated_backward(owq_layer_t gate, owq_layer_t up, int act, const uint16_t* x, const uint16_t* dh, uint16_t* dgate,
+                                uint16_t* dup, uint16_t* dx, int M, void* ws, size_t ws_bytes, owq_stream_t stream) {
+  Layer *g, *u;
+  owq_status_t st = lookup_pair(gate, up, &g, &u);
+  if (st) return st;
+  if (act < OWQ_ACT_SILU || act > OWQ_ACT_GELU_TANH) return OWQ_ERR_ARG;
+  if (M < 1 || M > 65536) return OWQ_ERR_SHAPE;
+  if (!x || !dh || !dgate || !dup || !dx || !ws) return OWQ_ERR_NULL;
+  if (!aligned16(x) || !aligned16(dh) || !aligned16(dgate) || !aligned16(dup) || !aligned16(dx) || !aligned16(ws)) return OWQ_ERR_ALIGN;
+  if ((st = check_pair_device(g, u))) return st;
+  return gated_backward_sm100(*g, *u, act, reinterpret_cast<const __half*>(x), reinterpret_cast<const __half*>(dh),
+                              reinterpret_cast<__half*>(dgate), reinterpret_cast<__half*>(dup), reinterpret_cast<__half*>(dx), M, ws,
+                              ws_bytes, kDefaultWaitLimit, reinterpret_cast<cudaStream_t>(stream));
 }
 
 owq_status_t owq_clip_create(const owq_grad_t* grads, int count, owq_stream_t stream, owq_clip_t* out) {

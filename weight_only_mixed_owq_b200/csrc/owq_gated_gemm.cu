@@ -90,6 +90,8 @@ struct GatedGemmParams {
   int k_ld[2];               // 0: no weak columns
   const __half* dh;          // NULL: forward
   __half* out[2];            // forward: h; backward: dg, du
+  __half* dy2[2];            // backward of few tokens: rows 2 t, 2 t + 1 = the gradients' halves of token t
+  int ld2;                   // (gated_store), zeros in columns N .. ld2 - 1; NULL: not wanted
   float* ws;                 // split partials
   int* status;
   int N, K, M, G, act;
@@ -100,15 +102,29 @@ struct GatedGemmParams {
   int skip_arrive;
 };
 
-// outputs of one element; gs, us: both projections; dhv: its gradient (BWD)
+// A gradient as the sum of two fp16 values, 22 bits of it, in rows 2 t and 2 t + 1
+__device__ __forceinline__ void store_halves(const GatedGemmParams& p, int l, int t, int row, float v) {
+  const __half hi = __float2half_rn(v);
+  const float lo = v - __half2float(hi);
+  __half* d = p.dy2[l] + (size_t)(2 * t) * p.ld2 + row;
+  d[0] = hi;
+  d[p.ld2] = __float2half_rn(__hisinf(hi) ? 0.f : lo);
+}
+
+// outputs of one element (token t, row); gs, us: both projections; dhv: its gradient (BWD)
 template <int ACT, bool BWD>
-__device__ __forceinline__ void gated_store(const GatedGemmParams& p, size_t o, float gs, float us, __half dhv) {
+__device__ __forceinline__ void gated_store(const GatedGemmParams& p, size_t o, int t, int row, float gs, float us, __half dhv) {
   float a, da;
   act_eval<ACT>(gs, a, da);
   if constexpr (BWD) {
     const float dh = __half2float(dhv);
-    p.out[0][o] = __float2half_rn(dh * us * da);
-    p.out[1][o] = __float2half_rn(dh * a);
+    const float dg = dh * us * da, du = dh * a;
+    p.out[0][o] = __float2half_rn(dg);
+    p.out[1][o] = __float2half_rn(du);
+    if (p.dy2[0]) {
+      store_halves(p, 0, t, row, dg);
+      store_halves(p, 1, t, row, du);
+    }
   } else {
     p.out[0][o] = __float2half_rn(a * us);
   }
@@ -143,7 +159,9 @@ __device__ __forceinline__ void gated_epilogue(const GatedGemmParams& p, uint32_
     for (int j = 0; j < 8; ++j) {
       const uint32_t got = __shfl_xor_sync(0xffffffffu, lay ? v[j] : v[j + 8], 16);
       const float gs = __uint_as_float(lay ? got : v[j]), us = __uint_as_float(lay ? v[j + 8] : got);
-      if (row_ok && first + c + j < p.M) gated_store<ACT, BWD>(p, o + (size_t)(c + j) * p.N, gs, us, dhv[j]);
+      const int t = first + c + j;
+      if (row_ok && t < p.M) gated_store<ACT, BWD>(p, o + (size_t)(c + j) * p.N, t, orow, gs, us, dhv[j]);
+      else if (BWD && p.dy2[0] && orow < p.ld2 && t < p.M) { store_halves(p, 0, t, orow, 0.f); store_halves(p, 1, t, orow, 0.f); }
     }
   }
 }
@@ -483,7 +501,10 @@ __global__ void k_gated_reduce(const __grid_constant__ GatedGemmParams p, int BN
     const int r = (int)(e % kHalfRows), t0 = (int)(e / kHalfRows % BN), u = (int)(e / kHalfRows / BN);
     const int tile = p.split.whole + u / 2, rank = u % 2;
     const int row = ((tile % p.rts) * 2 + rank) * kHalfRows + r, t = (tile / p.rts) * BN + t0;
-    if (row >= p.N || t >= p.M) continue;
+    if (row >= p.N || t >= p.M) {
+      if (p.dy2[0] && row < p.ld2 && t < p.M) { store_halves(p, 0, t, row, 0.f); store_halves(p, 1, t, row, 0.f); }
+      continue;
+    }
     const float* w = p.ws + partial_at(p.split, 0, tile, rank, BN) + (size_t)t0 * kBM + 32 * (r / 16) + r % 16;
     float gs = 0.f, us = 0.f;
     for (int z0 = 0; z0 < p.split.splits; z0 += 8) {   // eight splits' loads in flight
@@ -503,8 +524,8 @@ __global__ void k_gated_reduce(const __grid_constant__ GatedGemmParams p, int BN
     const size_t o = (size_t)t * p.N + row;
     with_act(p.act, [&](auto act) {
       constexpr int A = decltype(act)::value;
-      if (p.dh) gated_store<A, true>(p, o, gs, us, p.dh[o]);
-      else gated_store<A, false>(p, o, gs, us, __float2half_rn(0.f));
+      if (p.dh) gated_store<A, true>(p, o, t, row, gs, us, p.dh[o]);
+      else gated_store<A, false>(p, o, t, row, gs, us, __float2half_rn(0.f));
     });
   }
 }
@@ -532,6 +553,7 @@ struct GatedIgParams {
   int N, K, M, group;
   TileSplit split;  // tile = token tile * ceil(K / 256) + pair of column blocks; steps: 128 rows, the gate's first
   long long wait_limit;
+  int halves;           // tokens 2 t, 2 t + 1 are the halves of token t's gradients: dx's row t is their sum
   const float* wk[2];   // the weak columns' products, [row split][slot][M]
   const int32_t* idx[2];
   int k[2], wsplits;
@@ -784,9 +806,16 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
           for (int tk = 0; tk < 16; ++tk) w[tk * kBM] = __uint_as_float(v[tk]);
         }
       } else {
-        #pragma unroll
-        for (int tk = 0; tk < 16; ++tk)
-          sts_u16(smem_u32(s_out) + 2 * ((c0 + tk) * kStepCodes + j), __half_as_ushort(__float2half_rn(__uint_as_float(v[tk]))));
+        if (p.halves) {
+          #pragma unroll
+          for (int tk = 0; tk < 16; tk += 2)
+            sts_u16(smem_u32(s_out) + 2 * ((c0 + tk) / 2 * kStepCodes + j),
+                    __half_as_ushort(__float2half_rn(__uint_as_float(v[tk]) + __uint_as_float(v[tk + 1]))));
+        } else {
+          #pragma unroll
+          for (int tk = 0; tk < 16; ++tk)
+            sts_u16(smem_u32(s_out) + 2 * ((c0 + tk) * kStepCodes + j), __half_as_ushort(__float2half_rn(__uint_as_float(v[tk]))));
+        }
       }
     }
     if (to.n_splits == 1) {
@@ -817,18 +846,20 @@ __global__ void k_gated_ig_reduce(const __grid_constant__ GatedIgParams p, int B
   for (size_t e = 4 * ((size_t)blockIdx.x * blockDim.x + threadIdx.x); e < n; e += 4 * (size_t)gridDim.x * blockDim.x) {
     const int c = (int)(e % kBM), t0 = (int)(e / kBM % BN), u = (int)(e / kBM / BN), tile = p.split.whole + u / 2;
     const int b = (tile % Kp) * 2 + u % 2, t = (tile / Kp) * BN + t0;
-    if (t >= p.M || b >= Kb) continue;
+    if (t >= p.M || b >= Kb || (p.halves && (t & 1))) continue;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int z0 = 0; z0 < p.split.splits; z0 += 8) {   // eight splits' loads in flight
-      float4 w[8];
-      #pragma unroll
-      for (int z = 0; z < 8; ++z)
-        w[z] = z0 + z < p.split.splits ? *reinterpret_cast<const float4*>(p.ws + (size_t)(z0 + z) * n + e)
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-      #pragma unroll
-      for (int z = 0; z < 8; ++z) { v.x += w[z].x; v.y += w[z].y; v.z += w[z].z; v.w += w[z].w; }
+    for (int h = 0; h <= p.halves; ++h) {
+      for (int z0 = 0; z0 < p.split.splits; z0 += 8) {   // eight splits' loads in flight
+        float4 w[8];
+        #pragma unroll
+        for (int z = 0; z < 8; ++z)
+          w[z] = z0 + z < p.split.splits ? *reinterpret_cast<const float4*>(p.ws + (size_t)(z0 + z) * n + e + h * kBM)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+        #pragma unroll
+        for (int z = 0; z < 8; ++z) { v.x += w[z].x; v.y += w[z].y; v.z += w[z].z; v.w += w[z].w; }
+      }
     }
-    __half2* o = reinterpret_cast<__half2*>(dx + (size_t)t * p.K + b * kStepCodes + c);
+    __half2* o = reinterpret_cast<__half2*>(dx + (size_t)(t >> p.halves) * p.K + b * kStepCodes + c);
     o[0] = __floats2half2_rn(v.x, v.y);
     o[1] = __floats2half2_rn(v.z, v.w);
   }
@@ -1019,6 +1050,8 @@ struct FwdPlan {
   int BN, rts;
   TileSplit split;
   size_t xw[2], ws, total;  // byte offsets
+  __half* dy2[2] = {nullptr, nullptr};   // see GatedGemmParams
+  int ld2 = 0;
 };
 FwdPlan fwd_plan(const Layer& gate, const Layer& up, int M) {
   FwdPlan f;
@@ -1065,6 +1098,9 @@ owq_status_t run_gemm(const Layer& gate, const Layer& up, int act, const __half*
   prm.dh = dh;
   prm.out[0] = out0;
   prm.out[1] = out1;
+  prm.dy2[0] = f.dy2[0];
+  prm.dy2[1] = f.dy2[1];
+  prm.ld2 = f.ld2;
   prm.status = gate.status;
   prm.N = gate.N; prm.K = gate.K; prm.M = M; prm.G = gate.G; prm.act = act;
   prm.wait_limit = wait_limit; prm.skip_arrive = skip_arrive ? 1 : 0;
@@ -1123,16 +1159,19 @@ struct IgPlan {
   TileSplit split;
   int ldy, ct, wsplits, wper;   // weak products: slots of a tile, row splits, rows of a split
   size_t pad[2], wk[2], ws, total;
+  bool halves;   // of each token's gradients two rows, already padded
 };
-IgPlan ig_plan(const Layer& gate, const Layer& up, int M) {
+IgPlan ig_plan(const Layer& gate, const Layer& up, int tokens, bool halves = false) {
   IgPlan f;
+  const int M = halves ? 2 * tokens : tokens;
+  f.halves = halves;
   const int sms = layer_sm_count(gate.device);
   f.BN = pick_tile(M, (gate.K / kStepCodes + 1) / 2, 2 * ((gate.N + 127) / 128), sms, ig_cost, f.split);
   f.ldy = (gate.N + 7) & ~7;
   size_t at = 0;
   for (int l = 0; l < 2; ++l) {
     f.pad[l] = at;
-    if (gate.N % 8) at += up256((size_t)M * f.ldy * sizeof(__half));
+    if (gate.N % 8 && !halves) at += up256((size_t)M * f.ldy * sizeof(__half));
   }
   // weak products: up to three CTAs per SM; at least 4 chunks of rows and at most kIwMaxSplits splits
   // (the input gradient's epilogue adds them)
@@ -1163,11 +1202,12 @@ cudaError_t launch_igw(const GatedIgwArgs& a, dim3 grid, int device, cudaStream_
 }
 
 template <int BITS, int BN>
-owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const __half* du, __half* dx, int M, const IgPlan& f,
+owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const __half* du, __half* dx, int tokens, const IgPlan& f,
                     unsigned char* ws, long long wait_limit, cudaStream_t s) {
+  const int M = f.halves ? 2 * tokens : tokens;
   const Layer* L[2] = {&gate, &up};
   const __half* dy[2] = {dg, du};
-  if (gate.N % 8) {
+  if (gate.N % 8 && !f.halves) {
     __half* pad[2] = {reinterpret_cast<__half*>(ws + f.pad[0]), reinterpret_cast<__half*>(ws + f.pad[1])};
     k_gated_pad<<<blocks_for((size_t)M * f.ldy, 256, 4096), 256, 0, s>>>(dg, du, gate.N, f.ldy, (size_t)M, pad[0], pad[1]);
     if (cudaGetLastError() != cudaSuccess) return OWQ_ERR_CUDA;
@@ -1192,7 +1232,7 @@ owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const 
     wa.w[l] = L[l]->w_weak;
     wa.k_ld[l] = L[l]->k_ld;
   }
-  if (!encode_2d(&maps.dx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dx, (uint64_t)gate.K, (uint64_t)M, (uint64_t)gate.K * 2, kStepCodes, BN,
+  if (!encode_2d(&maps.dx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dx, (uint64_t)gate.K, (uint64_t)tokens, (uint64_t)gate.K * 2, kStepCodes, BN,
                  CU_TENSOR_MAP_SWIZZLE_NONE))
     return OWQ_ERR_CUDA;
   prm.status = gate.status;
@@ -1200,6 +1240,7 @@ owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const 
   prm.split = f.split;
   prm.wait_limit = wait_limit;
   prm.wsplits = f.wsplits;
+  prm.halves = f.halves ? 1 : 0;
   prm.ws = reinterpret_cast<float*>(ws + f.ws);
   wa.ctiles0 = (gate.k + f.ct - 1) / f.ct;
   wa.N = gate.N; wa.ldy = f.ldy; wa.M = M; wa.per = f.wper;
@@ -1259,6 +1300,46 @@ bool encode_gated_maps(Layer& L) {
       return false;
   }
   return true;
+}
+
+// The whole backward pass.  Up to kHalvesM tokens dx is formed from both halves of dgate and dup, twice
+// as many tokens in a tile that has room for them: its error is then that of its own rounding, where
+// the rounding of dgate and dup adds as much again (2.1e-4 and 2.9e-4 relative over many tokens, but
+// up to 1.6 times the former over one).  Beyond that it takes them as they are returned.
+namespace {
+constexpr int kHalvesM = 32;
+struct BwdPlan {
+  FwdPlan f;
+  IgPlan g;
+  size_t dy2[2], total;
+};
+BwdPlan bwd_plan(const Layer& gate, const Layer& up, int M) {
+  const bool halves = M <= kHalvesM;
+  BwdPlan b = {fwd_plan(gate, up, M), ig_plan(gate, up, M, halves), {0, 0}, 0};
+  b.total = std::max(b.f.total, b.g.total);
+  for (int l = 0; l < 2 && halves; ++l) {
+    b.dy2[l] = b.total;
+    b.total += up256((size_t)2 * M * b.g.ldy * sizeof(__half));
+  }
+  return b;
+}
+}  // namespace
+size_t gated_backward_ws_bytes(const Layer& gate, const Layer& up, int M) { return bwd_plan(gate, up, M).total; }
+owq_status_t gated_backward_sm100(const Layer& gate, const Layer& up, int act, const __half* x, const __half* dh, __half* dg,
+                                  __half* du, __half* dx, int M, void* ws, size_t ws_bytes, long long wait_limit, cudaStream_t s) {
+  BwdPlan b = bwd_plan(gate, up, M);
+  if (b.total > ws_bytes) return OWQ_ERR_NOMEM;
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  const __half* dy[2] = {dg, du};
+  if (b.g.halves) {
+    b.f.ld2 = b.g.ldy;
+    for (int l = 0; l < 2; ++l) dy[l] = b.f.dy2[l] = reinterpret_cast<__half*>(w + b.dy2[l]);
+  }
+  const owq_status_t st = gate.bits == 3 ? dispatch_gemm<3>(gate, up, act, x, dh, dg, du, M, b.f, w, wait_limit, false, s)
+                                         : dispatch_gemm<4>(gate, up, act, x, dh, dg, du, M, b.f, w, wait_limit, false, s);
+  if (st) return st;
+  return gate.bits == 3 ? dispatch_ig<3>(gate, up, dy[0], dy[1], dx, M, b.g, w, wait_limit, s)
+                        : dispatch_ig<4>(gate, up, dy[0], dy[1], dx, M, b.g, w, wait_limit, s);
 }
 
 size_t gated_gemm_ws_bytes(const Layer& gate, const Layer& up, int M) { return fwd_plan(gate, up, M).total; }

@@ -203,6 +203,10 @@ owq_status_t gated_gemm_sm100(const Layer& gate, const Layer& up, int act, const
 size_t gated_input_grad_ws_bytes(const Layer& gate, const Layer& up, int M);
 owq_status_t gated_input_grad_sm100(const Layer& gate, const Layer& up, const __half* dg, const __half* du, __half* dx, int M,
                                     void* ws, size_t ws_bytes, long long wait_limit, cudaStream_t s);
+// both, dx from the unrounded gradients up to 32 tokens
+size_t gated_backward_ws_bytes(const Layer& gate, const Layer& up, int M);
+owq_status_t gated_backward_sm100(const Layer& gate, const Layer& up, int act, const __half* x, const __half* dh, __half* dg,
+                                  __half* du, __half* dx, int M, void* ws, size_t ws_bytes, long long wait_limit, cudaStream_t s);
 // SM count of device `dev` (cached per device ordinal)
 int layer_sm_count(int dev);
 // Raise a kernel's dynamic shared memory limit, once per device (a bit of `done` each; the caller
