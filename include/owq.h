@@ -436,8 +436,9 @@ owq_status_t owq_gated_input_grad(owq_layer_t gate, owq_layer_t up, const uint16
 
 /*
  * owq_gated_backward -- the whole backward pass: owq_gated_grad, then dx (M x K).  Up to 32 tokens dx
- * is formed from dgate and dup before their rounding (22 bits of them), so that it carries its own
- * rounding only; beyond, it is owq_gated_input_grad of the returned dgate and dup, bit for bit.
+ * is formed from dgate and dup before their rounding (each as two fp16 values, hi + 2^-11 lo, off by at
+ * most 2^-22 of the value or 2^-36), so that it carries its own rounding only; beyond, it is
+ * owq_gated_input_grad of the returned dgate and dup, bit for bit.
  */
 owq_status_t owq_gated_backward(owq_layer_t gate, owq_layer_t up, int act, const uint16_t* x,
                                 const uint16_t* dh, uint16_t* dgate, uint16_t* dup, uint16_t* dx,

@@ -102,13 +102,16 @@ struct GatedGemmParams {
   int skip_arrive;
 };
 
-// A gradient as the sum of two fp16 values, 22 bits of it, in rows 2 t and 2 t + 1
+// A gradient as hi + 2^-11 lo, two fp16 values, in rows 2 t and 2 t + 1: hi its rounding, lo what that
+// left times 2^11, exact in fp32 and at most |v|, so that it neither overflows nor (unscaled, it would from
+// |v| < 2^-3 on) falls below fp16's normal range.  Off by at most 2^-22 |v|, or 2^-36.
+constexpr float kLoScale = 2048.f;
 __device__ __forceinline__ void store_halves(const GatedGemmParams& p, int l, int t, int row, float v) {
   const __half hi = __float2half_rn(v);
   const float lo = v - __half2float(hi);
   __half* d = p.dy2[l] + (size_t)(2 * t) * p.ld2 + row;
   d[0] = hi;
-  d[p.ld2] = __float2half_rn(__hisinf(hi) ? 0.f : lo);
+  d[p.ld2] = __float2half_rn(__hisinf(hi) ? 0.f : lo * kLoScale);
 }
 
 // outputs of one element (token t, row); gs, us: both projections; dhv: its gradient (BWD)
@@ -553,7 +556,7 @@ struct GatedIgParams {
   int N, K, M, group;
   TileSplit split;  // tile = token tile * ceil(K / 256) + pair of column blocks; steps: 128 rows, the gate's first
   long long wait_limit;
-  int halves;           // tokens 2 t, 2 t + 1 are the halves of token t's gradients: dx's row t is their sum
+  int halves;           // tokens 2 t, 2 t + 1 are hi and lo of token t's gradients: dx's row t is hi's + 2^-11 lo's
   const float* wk[2];   // the weak columns' products, [row split][slot][M]
   const int32_t* idx[2];
   int k[2], wsplits;
@@ -810,7 +813,7 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
           #pragma unroll
           for (int tk = 0; tk < 16; tk += 2)
             sts_u16(smem_u32(s_out) + 2 * ((c0 + tk) / 2 * kStepCodes + j),
-                    __half_as_ushort(__float2half_rn(__uint_as_float(v[tk]) + __uint_as_float(v[tk + 1]))));
+                    __half_as_ushort(__float2half_rn(fmaf(__uint_as_float(v[tk + 1]), 1.f / kLoScale, __uint_as_float(v[tk])))));
         } else {
           #pragma unroll
           for (int tk = 0; tk < 16; ++tk)
@@ -848,7 +851,7 @@ __global__ void k_gated_ig_reduce(const __grid_constant__ GatedIgParams p, int B
     const int b = (tile % Kp) * 2 + u % 2, t = (tile / Kp) * BN + t0;
     if (t >= p.M || b >= Kb || (p.halves && (t & 1))) continue;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int h = 0; h <= p.halves; ++h) {
+    for (int h = p.halves; h >= 0; --h) {   // lo's products first
       for (int z0 = 0; z0 < p.split.splits; z0 += 8) {   // eight splits' loads in flight
         float4 w[8];
         #pragma unroll
@@ -858,6 +861,7 @@ __global__ void k_gated_ig_reduce(const __grid_constant__ GatedIgParams p, int B
         #pragma unroll
         for (int z = 0; z < 8; ++z) { v.x += w[z].x; v.y += w[z].y; v.z += w[z].z; v.w += w[z].w; }
       }
+      if (h) { v.x *= 1.f / kLoScale; v.y *= 1.f / kLoScale; v.z *= 1.f / kLoScale; v.w *= 1.f / kLoScale; }
     }
     __half2* o = reinterpret_cast<__half2*>(dx + (size_t)(t >> p.halves) * p.K + b * kStepCodes + c);
     o[0] = __floats2half2_rn(v.x, v.y);
