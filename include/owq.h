@@ -59,6 +59,7 @@ typedef int owq_status_t;
 #define OWQ_INJECT_GEMV_TAG     1
 #define OWQ_INJECT_GEMM_ARRIVE  2
 #define OWQ_INJECT_BOUNDS       3
+#define OWQ_INJECT_CLIP         4
 
 /* Opaque handle of one packed layer; owns the device buffers owq_pack allocated. */
 typedef struct owq_layer_s* owq_layer_t;
@@ -534,6 +535,9 @@ owq_status_t owq_device_status(void);
  *                           its column; the bounds check skips that store and the next
  *                           owq_device_status returns OWQ_ERR_BOUNDS (dx[0][idx[0]] is then
  *                           undefined, every other output as without the injection).
+ *   OWQ_INJECT_CLIP         next owq_clip_grads: CTA 0 never copies its first chunk, so its waits for it
+ *                           run out, and it publishes its sum after the others' waits for it have run
+ *                           out; the norm and the outputs are then undefined.
  * OWQ_INJECT_NONE disarms (wait_cycles ignored).  Errors: OWQ_ERR_ARG for an unknown `what`
  * or wait_cycles < 1.
  */

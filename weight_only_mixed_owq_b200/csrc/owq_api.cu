@@ -455,7 +455,8 @@ owq_status_t owq_debug_inject(int what, long long wait_cycles) {
     g_inject = what;
     return OWQ_OK;
   }
-  if ((what != OWQ_INJECT_GEMV_TAG && what != OWQ_INJECT_GEMM_ARRIVE) || wait_cycles < 1) return OWQ_ERR_ARG;
+  if ((what != OWQ_INJECT_GEMV_TAG && what != OWQ_INJECT_GEMM_ARRIVE && what != OWQ_INJECT_CLIP) || wait_cycles < 1)
+    return OWQ_ERR_ARG;
   g_inject = what;
   g_inject_wait = wait_cycles;
   return OWQ_OK;
@@ -739,7 +740,9 @@ owq_status_t owq_clip_grads(owq_clip_t clip, float max_norm, float* norm, owq_st
   if (!aligned16(norm)) return OWQ_ERR_ALIGN;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev != c->device) { cudaGetLastError(); return OWQ_ERR_DEVICE; }
-  return cuda_status(launch_clip(*c, max_norm, norm, kDefaultWaitLimit, reinterpret_cast<cudaStream_t>(stream)));
+  long long wl;
+  const bool skip = take_inject(OWQ_INJECT_CLIP, &wl);
+  return cuda_status(launch_clip(*c, max_norm, norm, wl, skip, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 owq_status_t owq_clip_free(owq_clip_t clip) {

@@ -46,6 +46,7 @@ struct ClipArgs {
   float* norm;
   int* status;
   long long wait_limit;
+  int skip;                      // test-injected: CTA 0 never copies its first chunk and publishes late
 };
 
 template <int DT>
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) k_clip(const __grid_constant
   __shared__ ClipChunk s_chunk[kMaxSlots];
   __shared__ uint64_t full[kMaxSlots], empty[kMaxSlots];
   __shared__ double s_red[kWarps];
-  __shared__ int s_ok;
+  __shared__ int s_ok, s_lost;   // the grid's barrier was passed; a warp's wait in the first pass gave up
   const int G = gridDim.x, b = blockIdx.x, S = a.slots, lane = threadIdx.x & 31;
   const int mine = b < a.n_chunks ? (a.n_chunks - 1 - b) / G + 1 : 0;   // chunks b, b + G, ...
   const Uses uses{mine, S};
@@ -183,6 +184,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) k_clip(const __grid_constant
       mbar_init(&empty[i], kWarps);
     }
     fence_mbar_init();
+    s_lost = 0;
   }
   __syncthreads();
 
@@ -190,6 +192,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) k_clip(const __grid_constant
     // ---------------- producer ----------------
     // one lane copies; the warp fetches the table entries 32 at a time
     bool ok = true;
+    int copies = 0;   // lane s: copies issued into slot s
     ClipChunk mineq = {};
     uint64_t first;   // evict first: what the second pass will not find in L2 anyway, or has read
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
@@ -216,22 +219,26 @@ __global__ void __launch_bounds__(kThreads + 32, 1) k_clip(const __grid_constant
       if (i % 32 == 0 && i + lane < mine) mineq = a.chunks[b + (size_t)(i + lane) * G];
       const ClipChunk c = entry(i % 32);
       if (i >= S) ok = __all_sync(0xffffffffu, mbar_wait(&empty[i % S], (uint32_t)(i / S - 1) & 1, a.status, a.wait_limit));
-      if (ok && lane == 0) load(i, c, i >= mine - a.keep);
+      const bool skip = a.skip && b == 0 && i == 0;
+      if (ok && !skip && lane == 0) load(i, c, i >= mine - a.keep);
+      if (ok && !skip && lane == i % S) ++copies;
       __syncwarp();
     }
     // Every slot's first-pass uses are consumed before the second pass waits on the slots' barriers: a
     // wait by parity must not be more than one phase ahead of its barrier.
     named_bar_sync(2, kThreads + 32);
+    ok = ok && !s_lost;   // (their uses were not all consumed: there is no second pass)
     for (int k = 0, i = mine - S - 1; i >= 0 && ok; --i, ++k) {   // the second pass, after the resident chunks
       if (k % 32 == 0 && i - lane >= 0) mineq = a.chunks[b + (size_t)(i - lane) * G];
       const ClipChunk c = entry(k % 32);
       // the second pass's use of the slot by chunk i + S is over: its consumption follows the first pass's
       ok = __all_sync(0xffffffffu, mbar_wait(&empty[i % S], (uint32_t)uses.second(i) & 1, a.status, a.wait_limit));
       if (ok && lane == 0) load(i, c, false);
+      if (ok && lane == i % S) ++copies;
       __syncwarp();
     }
-    // never leave with copies in flight: the last copy into every slot
-    if (lane < min(S, mine)) mbar_wait(&full[lane], (uint32_t)(mine > S ? uses.second(lane) : 0) & 1, a.status, a.wait_limit);
+    // never leave with copies in flight: the last one issued into every slot
+    if (copies > 0) mbar_wait(&full[lane], (uint32_t)(copies - 1) & 1, a.status, a.wait_limit);
     return;
   }
 
@@ -251,11 +258,14 @@ __global__ void __launch_bounds__(kThreads + 32, 1) k_clip(const __grid_constant
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[sl]);
   }
+  if (!ok && lane == 0) s_lost = 1;
   named_bar_sync(2, kThreads + 32);   // the producer's second pass may start
   s = block_sum(s, s_red);
 
   // publish, then wait until every CTA of this call has: the counter only grows, by G a call
   if (threadIdx.x == 0) {
+    if (a.skip && b == 0)
+      for (const long long t0 = clock64(); clock64() - t0 < 2 * a.wait_limit;) {}
     a.part[b] = s;
     __threadfence();
     const unsigned long long old = atomicAdd(a.arrived, 1ull);
@@ -269,10 +279,10 @@ __global__ void __launch_bounds__(kThreads + 32, 1) k_clip(const __grid_constant
         break;
       }
     __threadfence();
-    s_ok = all;
+    s_ok = all && !s_lost;
   }
   named_bar_sync(1, kThreads);
-  ok = ok && s_ok;
+  ok = s_ok;   // (of all warps together)
   double t = 0.0;
   for (int i = threadIdx.x; i < G; i += kThreads) t += __ldcg(a.part + i);
   t = block_sum(t, s_red);
@@ -280,12 +290,14 @@ __global__ void __launch_bounds__(kThreads + 32, 1) k_clip(const __grid_constant
   const float f = norm <= 3.402823466e38f ? fminf(a.max_norm / (norm + 1e-6f), 1.f) : 1.f;   // (false for NaN too)
   if (b == 0 && threadIdx.x == 0 && ok) *a.norm = norm;
 
-  for (int i = mine - 1; i >= 0; --i) {
+  // (a warp whose wait gave up stops: an arrival of its own for a later use of a slot could stand in for
+  // another warp's, and the slot and its table entry be replaced under that one)
+  for (int i = mine - 1; i >= 0 && ok; --i) {
     const int sl = i % S;
-    if (i < mine - S && ok) ok = __all_sync(0xffffffffu, mbar_wait(&full[sl], (uint32_t)uses.second(i) & 1, a.status, a.wait_limit));
+    if (i < mine - S && !(ok = __all_sync(0xffffffffu, mbar_wait(&full[sl], (uint32_t)uses.second(i) & 1, a.status, a.wait_limit)))) break;
     const uint4* slot = reinterpret_cast<const uint4*>(ring + (size_t)sl * a.slot_bytes);
     const ClipChunk c = s_chunk[sl];
-    if (ok && !(f == 1.f && c.in == c.out)) {   // (in place and unclipped: nothing to write)
+    if (!(f == 1.f && c.in == c.out)) {   // (in place and unclipped: nothing to write)
       if (c.dtype == OWQ_F32) scale<OWQ_F32>(c, slot, f);
       else if (c.dtype == OWQ_F16) scale<OWQ_F16>(c, slot, f);
       else scale<OWQ_BF16>(c, slot, f);
@@ -304,8 +316,9 @@ int clip_chunk_bytes(long long total_bytes, int sms) {
   return (int)std::max<long long>(4096, std::min<long long>(kChunkBytes, (want + 4095) / 4096 * 4096));
 }
 
-cudaError_t launch_clip(const Clip& c, float max_norm, float* norm, long long wait_limit, cudaStream_t s) {
+cudaError_t launch_clip(const Clip& c, float max_norm, float* norm, long long wait_limit, bool skip, cudaStream_t s) {
   ClipArgs a;
+  a.skip = skip ? 1 : 0;
   a.chunks = c.chunks;
   a.n_chunks = c.n_chunks;
   a.slot_bytes = c.chunk_bytes;

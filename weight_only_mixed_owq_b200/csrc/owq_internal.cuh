@@ -228,6 +228,6 @@ struct Clip {
   unsigned long long* arrived;   // CTAs that have published their sum, over all calls
 };
 int clip_chunk_bytes(long long total_bytes, int sms);
-cudaError_t launch_clip(const Clip& c, float max_norm, float* norm, long long wait_limit, cudaStream_t s);
+cudaError_t launch_clip(const Clip& c, float max_norm, float* norm, long long wait_limit, bool skip, cudaStream_t s);
 
 }  // namespace owq
