@@ -60,6 +60,7 @@ typedef int owq_status_t;
 #define OWQ_INJECT_GEMM_ARRIVE  2
 #define OWQ_INJECT_BOUNDS       3
 #define OWQ_INJECT_CLIP         4
+#define OWQ_INJECT_GATED        5
 
 /* Opaque handle of one packed layer; owns the device buffers owq_pack allocated. */
 typedef struct owq_layer_s* owq_layer_t;
@@ -525,8 +526,9 @@ owq_status_t owq_device_status(void);
  *   OWQ_INJECT_GEMM_ARRIVE  next owq_gemm or owq_gated_gemm: one dequantisation thread of every CTA skips its
  *                           arrival for its first K step, so the MMA issuer's wait runs out,
  *                           then the producer's and the dequantisation threads' waits.
- * wait_cycles (>= 1) bounds every device wait of that call, in SM clock cycles (otherwise the
- * bound is 4e9 cycles, about 2 s).  The kernel records the timeout in the device status
+ * wait_cycles (>= 1; at least 200000 are taken, so that copies and products in flight end within
+ * the waits that follow one that gave up) bounds every device wait of that call, in SM clock cycles
+ * (otherwise the bound is 4e9 cycles, about 2 s).  The kernel records the timeout in the device status
  * word, leaves y undefined, lets its own bulk copies land, frees its tensor memory and
  * returns: the next owq_device_status returns OWQ_ERR_TIMEOUT and the context stays usable.
  *   OWQ_INJECT_BOUNDS       debug-bounds build only (OWQ_ERR_ARG otherwise; wait_cycles ignored):
@@ -538,6 +540,10 @@ owq_status_t owq_device_status(void);
  *   OWQ_INJECT_CLIP         next owq_clip_grads: CTA 0 never copies its first chunk, so its waits for it
  *                           run out, and it publishes its sum after the others' waits for it have run
  *                           out; the norm and the outputs are then undefined.
+ *   OWQ_INJECT_GATED        next owq_gated_gemv: every CTA holds back an arrival for its activations in shared
+ *                           memory (those that stay in global memory are not waited for); next owq_gated_gemm,
+ *                           owq_gated_grad, owq_gated_input_grad, owq_gated_backward (both its
+ *                           products): the skipped arrivals of OWQ_INJECT_GEMM_ARRIVE.
  * OWQ_INJECT_NONE disarms (wait_cycles ignored).  Errors: OWQ_ERR_ARG for an unknown `what`
  * or wait_cycles < 1.
  */

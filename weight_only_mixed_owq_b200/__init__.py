@@ -8,7 +8,7 @@ script, `weight_only_mixed_owq_b200.build`, imports without the library.
 import importlib
 
 _EXPORTS = (
-    "LIB", "LIB_PATH", "OWQ_OK", "OWQ_INJECT_NONE", "OWQ_INJECT_GEMV_TAG", "OWQ_INJECT_GEMM_ARRIVE", "OWQ_INJECT_BOUNDS", "OWQ_INJECT_CLIP",
+    "LIB", "LIB_PATH", "OWQ_OK", "OWQ_INJECT_NONE", "OWQ_INJECT_GEMV_TAG", "OWQ_INJECT_GEMM_ARRIVE", "OWQ_INJECT_BOUNDS", "OWQ_INJECT_CLIP", "OWQ_INJECT_GATED",
     "OwqError", "OwqGated", "OwqGrad", "OwqGradClip", "OwqLayer", "PROTOTYPES", "STATUS_NAMES",
     "OWQ_ACT_SILU", "OWQ_ACT_GELU", "OWQ_ACT_GELU_TANH", "OWQ_F32", "OWQ_F16", "OWQ_BF16",
     "clip_grads", "owq_clip_create", "owq_clip_free", "owq_clip_grads",

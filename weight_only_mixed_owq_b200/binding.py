@@ -25,7 +25,8 @@ STATUS_NAMES = {
 }
 OWQ_ACT_SILU, OWQ_ACT_GELU, OWQ_ACT_GELU_TANH = 0, 1, 2
 OWQ_F32, OWQ_F16, OWQ_BF16 = 0, 1, 2
-OWQ_INJECT_NONE, OWQ_INJECT_GEMV_TAG, OWQ_INJECT_GEMM_ARRIVE, OWQ_INJECT_BOUNDS, OWQ_INJECT_CLIP = 0, 1, 2, 3, 4
+OWQ_INJECT_NONE, OWQ_INJECT_GEMV_TAG, OWQ_INJECT_GEMM_ARRIVE, OWQ_INJECT_BOUNDS = 0, 1, 2, 3
+OWQ_INJECT_CLIP, OWQ_INJECT_GATED = 4, 5
 
 # (name, restype, argtypes) of every exported symbol of include/owq.h
 _P, _I, _SZ, _S = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t), ctypes.c_char_p

@@ -438,6 +438,8 @@ owq_status_t owq_pack_storage(const uint32_t* words, int N, int K, int bits, int
 // one armed test failure (owq_debug_inject), taken by the next call of its kind
 static int g_inject = OWQ_INJECT_NONE;
 static long long g_inject_wait = kDefaultWaitLimit;
+// about 0.1 ms: copies and MMAs that are in flight when a wait gives up have ended before the next one does
+constexpr long long kMinInjectWait = 200000;
 
 // wait bound of this call; true if the armed failure is of kind `what` (then disarmed)
 static bool take_inject(int what, long long* wait_limit) {
@@ -455,10 +457,11 @@ owq_status_t owq_debug_inject(int what, long long wait_cycles) {
     g_inject = what;
     return OWQ_OK;
   }
-  if ((what != OWQ_INJECT_GEMV_TAG && what != OWQ_INJECT_GEMM_ARRIVE && what != OWQ_INJECT_CLIP) || wait_cycles < 1)
+  if ((what != OWQ_INJECT_GEMV_TAG && what != OWQ_INJECT_GEMM_ARRIVE && what != OWQ_INJECT_CLIP && what != OWQ_INJECT_GATED) ||
+      wait_cycles < 1)
     return OWQ_ERR_ARG;
   g_inject = what;
-  g_inject_wait = wait_cycles;
+  g_inject_wait = std::max(wait_cycles, kMinInjectWait);
   return OWQ_OK;
 }
 
@@ -582,8 +585,10 @@ owq_status_t owq_gated_gemv(owq_layer_t gate, owq_layer_t up, int act, const uin
   if (!x || !h) return OWQ_ERR_NULL;
   if (!aligned16(x) || !aligned16(h)) return OWQ_ERR_ALIGN;
   if ((st = check_pair_device(g, u))) return st;
-  return cuda_status(launch_gated_gemv(*g, *u, act, reinterpret_cast<const __half*>(x), reinterpret_cast<__half*>(h), M,
-                                       kDefaultWaitLimit, reinterpret_cast<cudaStream_t>(stream)));
+  long long wl;
+  const bool skip = take_inject(OWQ_INJECT_GATED, &wl);
+  return cuda_status(launch_gated_gemv(*g, *u, act, reinterpret_cast<const __half*>(x), reinterpret_cast<__half*>(h), M, wl, skip,
+                                       reinterpret_cast<cudaStream_t>(stream)));
 }
 
 owq_status_t owq_gated_workspace(owq_layer_t gate, owq_layer_t up, int M, size_t* bytes) {
@@ -607,7 +612,7 @@ owq_status_t owq_gated_gemm(owq_layer_t gate, owq_layer_t up, int act, const uin
   if (!aligned16(x) || !aligned16(h) || !aligned16(ws)) return OWQ_ERR_ALIGN;
   if ((st = check_pair_device(g, u))) return st;
   long long wl;
-  const bool skip = take_inject(OWQ_INJECT_GEMM_ARRIVE, &wl);
+  const bool skip = take_inject(OWQ_INJECT_GEMM_ARRIVE, &wl) || take_inject(OWQ_INJECT_GATED, &wl);
   return gated_gemm_sm100(*g, *u, act, reinterpret_cast<const __half*>(x), nullptr, reinterpret_cast<__half*>(h), nullptr, M, ws,
                           ws_bytes, wl, skip, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -622,9 +627,11 @@ owq_status_t owq_gated_grad(owq_layer_t gate, owq_layer_t up, int act, const uin
   if (!x || !dh || !dgate || !dup || !ws) return OWQ_ERR_NULL;
   if (!aligned16(x) || !aligned16(dh) || !aligned16(dgate) || !aligned16(dup) || !aligned16(ws)) return OWQ_ERR_ALIGN;
   if ((st = check_pair_device(g, u))) return st;
+  long long wl;
+  const bool skip = take_inject(OWQ_INJECT_GATED, &wl);
   return gated_gemm_sm100(*g, *u, act, reinterpret_cast<const __half*>(x), reinterpret_cast<const __half*>(dh),
-                          reinterpret_cast<__half*>(dgate), reinterpret_cast<__half*>(dup), M, ws, ws_bytes, kDefaultWaitLimit,
-                          false, reinterpret_cast<cudaStream_t>(stream));
+                          reinterpret_cast<__half*>(dgate), reinterpret_cast<__half*>(dup), M, ws, ws_bytes, wl, skip,
+                          reinterpret_cast<cudaStream_t>(stream));
 }
 
 owq_status_t owq_gated_input_grad(owq_layer_t gate, owq_layer_t up, const uint16_t* dgate, const uint16_t* dup, uint16_t* dx,
@@ -636,9 +643,10 @@ owq_status_t owq_gated_input_grad(owq_layer_t gate, owq_layer_t up, const uint16
   if (!dgate || !dup || !dx || !ws) return OWQ_ERR_NULL;
   if (!aligned16(dgate) || !aligned16(dup) || !aligned16(dx) || !aligned16(ws)) return OWQ_ERR_ALIGN;
   if ((st = check_pair_device(g, u))) return st;
+  long long wl;
+  const bool skip = take_inject(OWQ_INJECT_GATED, &wl);
   return gated_input_grad_sm100(*g, *u, reinterpret_cast<const __half*>(dgate), reinterpret_cast<const __half*>(dup),
-                                reinterpret_cast<__half*>(dx), M, ws, ws_bytes, kDefaultWaitLimit,
-                                reinterpret_cast<cudaStream_t>(stream));
+                                reinterpret_cast<__half*>(dx), M, ws, ws_bytes, wl, skip, reinterpret_cast<cudaStream_t>(stream));
 }
 
 owq_status_t owq_gated_backward(owq_layer_t gate, owq_layer_t up, int act, const uint16_t* x, const uint16_t* dh, uint16_t* dgate,
@@ -651,9 +659,11 @@ owq_status_t owq_gated_backward(owq_layer_t gate, owq_layer_t up, int act, const
   if (!x || !dh || !dgate || !dup || !dx || !ws) return OWQ_ERR_NULL;
   if (!aligned16(x) || !aligned16(dh) || !aligned16(dgate) || !aligned16(dup) || !aligned16(dx) || !aligned16(ws)) return OWQ_ERR_ALIGN;
   if ((st = check_pair_device(g, u))) return st;
+  long long wl;
+  const bool skip = take_inject(OWQ_INJECT_GATED, &wl);
   return gated_backward_sm100(*g, *u, act, reinterpret_cast<const __half*>(x), reinterpret_cast<const __half*>(dh),
                               reinterpret_cast<__half*>(dgate), reinterpret_cast<__half*>(dup), reinterpret_cast<__half*>(dx), M, ws,
-                              ws_bytes, kDefaultWaitLimit, reinterpret_cast<cudaStream_t>(stream));
+                              ws_bytes, wl, skip, reinterpret_cast<cudaStream_t>(stream));
 }
 
 owq_status_t owq_clip_create(const owq_grad_t* grads, int count, owq_stream_t stream, owq_clip_t* out) {

@@ -556,6 +556,7 @@ struct GatedIgParams {
   int N, K, M, group;
   TileSplit split;  // tile = token tile * ceil(K / 256) + pair of column blocks; steps: 128 rows, the gate's first
   long long wait_limit;
+  int skip_arrive;
   int halves;           // tokens 2 t, 2 t + 1 are hi and lo of token t's gradients: dx's row t is hi's + 2^-11 lo's
   const float* wk[2];   // the weak columns' products, [row split][slot][M]
   const int32_t* idx[2];
@@ -737,7 +738,7 @@ k_gated_igemm(const __grid_constant__ GatedIgMaps maps, const __grid_constant__ 
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(&afull[i % kS2], 0);
+      if (lane == 0 && !(p.skip_arrive && i == 0 && threadIdx.x == 64)) mbar_arrive_remote(&afull[i % kS2], 0);
     }
 
     // ---------------- epilogue ----------------
@@ -1207,7 +1208,7 @@ cudaError_t launch_igw(const GatedIgwArgs& a, dim3 grid, int device, cudaStream_
 
 template <int BITS, int BN>
 owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const __half* du, __half* dx, int tokens, const IgPlan& f,
-                    unsigned char* ws, long long wait_limit, cudaStream_t s) {
+                    unsigned char* ws, long long wait_limit, bool skip_arrive, cudaStream_t s) {
   const int M = f.halves ? 2 * tokens : tokens;
   const Layer* L[2] = {&gate, &up};
   const __half* dy[2] = {dg, du};
@@ -1242,7 +1243,7 @@ owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const 
   prm.status = gate.status;
   prm.N = gate.N; prm.K = gate.K; prm.M = M; prm.group = gate.group;
   prm.split = f.split;
-  prm.wait_limit = wait_limit;
+  prm.wait_limit = wait_limit; prm.skip_arrive = skip_arrive ? 1 : 0;
   prm.wsplits = f.wsplits;
   prm.halves = f.halves ? 1 : 0;
   prm.ws = reinterpret_cast<float*>(ws + f.ws);
@@ -1286,12 +1287,12 @@ owq_status_t run_ig(const Layer& gate, const Layer& up, const __half* dg, const 
 
 template <int BITS>
 owq_status_t dispatch_ig(const Layer& gate, const Layer& up, const __half* dg, const __half* du, __half* dx, int M, const IgPlan& f,
-                         unsigned char* ws, long long wl, cudaStream_t s) {
+                         unsigned char* ws, long long wl, bool skip, cudaStream_t s) {
   switch (f.BN) {
-    case 64: return run_ig<BITS, 64>(gate, up, dg, du, dx, M, f, ws, wl, s);
-    case 192: return run_ig<BITS, 192>(gate, up, dg, du, dx, M, f, ws, wl, s);
-    case 128: return run_ig<BITS, 128>(gate, up, dg, du, dx, M, f, ws, wl, s);
-    default: return run_ig<BITS, 256>(gate, up, dg, du, dx, M, f, ws, wl, s);
+    case 64: return run_ig<BITS, 64>(gate, up, dg, du, dx, M, f, ws, wl, skip, s);
+    case 192: return run_ig<BITS, 192>(gate, up, dg, du, dx, M, f, ws, wl, skip, s);
+    case 128: return run_ig<BITS, 128>(gate, up, dg, du, dx, M, f, ws, wl, skip, s);
+    default: return run_ig<BITS, 256>(gate, up, dg, du, dx, M, f, ws, wl, skip, s);
   }
 }
 
@@ -1330,7 +1331,8 @@ BwdPlan bwd_plan(const Layer& gate, const Layer& up, int M) {
 }  // namespace
 size_t gated_backward_ws_bytes(const Layer& gate, const Layer& up, int M) { return bwd_plan(gate, up, M).total; }
 owq_status_t gated_backward_sm100(const Layer& gate, const Layer& up, int act, const __half* x, const __half* dh, __half* dg,
-                                  __half* du, __half* dx, int M, void* ws, size_t ws_bytes, long long wait_limit, cudaStream_t s) {
+                                  __half* du, __half* dx, int M, void* ws, size_t ws_bytes, long long wait_limit,
+                                  bool skip_arrive, cudaStream_t s) {
   BwdPlan b = bwd_plan(gate, up, M);
   if (b.total > ws_bytes) return OWQ_ERR_NOMEM;
   unsigned char* w = static_cast<unsigned char*>(ws);
@@ -1339,11 +1341,11 @@ owq_status_t gated_backward_sm100(const Layer& gate, const Layer& up, int act, c
     b.f.ld2 = b.g.ldy;
     for (int l = 0; l < 2; ++l) dy[l] = b.f.dy2[l] = reinterpret_cast<__half*>(w + b.dy2[l]);
   }
-  const owq_status_t st = gate.bits == 3 ? dispatch_gemm<3>(gate, up, act, x, dh, dg, du, M, b.f, w, wait_limit, false, s)
-                                         : dispatch_gemm<4>(gate, up, act, x, dh, dg, du, M, b.f, w, wait_limit, false, s);
+  const owq_status_t st = gate.bits == 3 ? dispatch_gemm<3>(gate, up, act, x, dh, dg, du, M, b.f, w, wait_limit, skip_arrive, s)
+                                         : dispatch_gemm<4>(gate, up, act, x, dh, dg, du, M, b.f, w, wait_limit, skip_arrive, s);
   if (st) return st;
-  return gate.bits == 3 ? dispatch_ig<3>(gate, up, dy[0], dy[1], dx, M, b.g, w, wait_limit, s)
-                        : dispatch_ig<4>(gate, up, dy[0], dy[1], dx, M, b.g, w, wait_limit, s);
+  return gate.bits == 3 ? dispatch_ig<3>(gate, up, dy[0], dy[1], dx, M, b.g, w, wait_limit, skip_arrive, s)
+                        : dispatch_ig<4>(gate, up, dy[0], dy[1], dx, M, b.g, w, wait_limit, skip_arrive, s);
 }
 
 size_t gated_gemm_ws_bytes(const Layer& gate, const Layer& up, int M) { return fwd_plan(gate, up, M).total; }
@@ -1360,12 +1362,12 @@ owq_status_t gated_gemm_sm100(const Layer& gate, const Layer& up, int act, const
 }
 
 owq_status_t gated_input_grad_sm100(const Layer& gate, const Layer& up, const __half* dg, const __half* du, __half* dx, int M,
-                                    void* ws, size_t ws_bytes, long long wait_limit, cudaStream_t s) {
+                                    void* ws, size_t ws_bytes, long long wait_limit, bool skip_arrive, cudaStream_t s) {
   const IgPlan f = ig_plan(gate, up, M);
   if (f.total > ws_bytes) return OWQ_ERR_NOMEM;
   unsigned char* w = static_cast<unsigned char*>(ws);
-  return gate.bits == 3 ? dispatch_ig<3>(gate, up, dg, du, dx, M, f, w, wait_limit, s)
-                        : dispatch_ig<4>(gate, up, dg, du, dx, M, f, w, wait_limit, s);
+  return gate.bits == 3 ? dispatch_ig<3>(gate, up, dg, du, dx, M, f, w, wait_limit, skip_arrive, s)
+                        : dispatch_ig<4>(gate, up, dg, du, dx, M, f, w, wait_limit, skip_arrive, s);
 }
 
 }  // namespace owq

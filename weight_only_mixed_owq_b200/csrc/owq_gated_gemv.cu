@@ -70,6 +70,7 @@ struct GatedGemvArgs {
   int o_bars, o_early, o_sz, o_idx, o_x;   // shared memory offsets
   int* status;
   long long wait_limit;
+  int skip;                     // test-injected: an arrival for the activations is held back in every CTA
   uint16_t idx16[2][kParamIdx]; // the first weak indices (a load would cost the prologue its latency)
 };
 
@@ -177,7 +178,7 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
   if (lane == 0) {
     for (int i = 0; i < S; ++i) mbar_init(&bars[i], 1);
     if (warp == 0) {
-      mbar_init(xbar, 1);
+      mbar_init(xbar, 1 + a.skip);
       mbar_init(wbar, kWarps);
     }
     fence_mbar_init();
@@ -410,7 +411,10 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
       }
     }
     if (!ok && lane == 0) {   // after a timeout: never exit with copies on their way into this CTA's memory
-      if (XSMEM && threadIdx.x == 0) mbar_wait(xbar, 0, a.status, a.wait_limit);
+      if (XSMEM && threadIdx.x == 0) {
+        if (a.skip) mbar_arrive(xbar);   // (the arrival that was held back)
+        mbar_wait(xbar, 0, a.status, a.wait_limit);
+      }
       for (; in_flight > 0; --in_flight) {
         mbar_wait(&bars[st], phase, a.status, a.wait_limit);
         if (++st == S) { st = 0; phase ^= 1u; }
@@ -555,8 +559,9 @@ cudaError_t launch_b(GatedGemvArgs& a, bool pg, int all, int sms, int dev, cudaS
 }  // namespace
 
 cudaError_t launch_gated_gemv(const Layer& gate, const Layer& up, int act, const __half* x, __half* h, int M,
-                              long long wait_limit, cudaStream_t s) {
+                              long long wait_limit, bool skip, cudaStream_t s) {
   GatedGemvArgs a{};
+  a.skip = skip ? 1 : 0;
   const Layer* L[2] = {&gate, &up};
   for (int l = 0; l < 2; ++l) {
     a.packed[l] = L[l]->packed;

@@ -192,7 +192,7 @@ owq_status_t gemm_sm100(Layer& L, const __half* x, __half* y, int M, long long w
 bool encode_gated_maps(Layer& L);
 // decode form, M <= kMaxGemvM: one launch, no workspace
 cudaError_t launch_gated_gemv(const Layer& gate, const Layer& up, int act, const __half* x, __half* h, int M,
-                              long long wait_limit, cudaStream_t s);
+                              long long wait_limit, bool skip, cudaStream_t s);
 // many tokens: h = act(g) u (dh NULL, out0 = h), or the gradients of both projections' outputs
 // (out0 = dg, out1 = du); ws: the caller's workspace of at least gated_gemm_ws_bytes
 size_t gated_gemm_ws_bytes(const Layer& gate, const Layer& up, int M);
@@ -202,11 +202,12 @@ owq_status_t gated_gemm_sm100(const Layer& gate, const Layer& up, int act, const
 // dx = dg Wg + du Wu
 size_t gated_input_grad_ws_bytes(const Layer& gate, const Layer& up, int M);
 owq_status_t gated_input_grad_sm100(const Layer& gate, const Layer& up, const __half* dg, const __half* du, __half* dx, int M,
-                                    void* ws, size_t ws_bytes, long long wait_limit, cudaStream_t s);
+                                    void* ws, size_t ws_bytes, long long wait_limit, bool skip_arrive, cudaStream_t s);
 // both, dx from the unrounded gradients up to 32 tokens
 size_t gated_backward_ws_bytes(const Layer& gate, const Layer& up, int M);
 owq_status_t gated_backward_sm100(const Layer& gate, const Layer& up, int act, const __half* x, const __half* dh, __half* dg,
-                                  __half* du, __half* dx, int M, void* ws, size_t ws_bytes, long long wait_limit, cudaStream_t s);
+                                  __half* du, __half* dx, int M, void* ws, size_t ws_bytes, long long wait_limit,
+                                  bool skip_arrive, cudaStream_t s);
 // SM count of device `dev` (cached per device ordinal)
 int layer_sm_count(int dev);
 // Raise a kernel's dynamic shared memory limit, once per device (a bit of `done` each; the caller
