@@ -409,6 +409,25 @@ owq_status_t owq_gated_gemv(owq_layer_t gate, owq_layer_t up, int act, const uin
 owq_status_t owq_gated_workspace(owq_layer_t gate, owq_layer_t up, int M, size_t* bytes);
 
 /*
+ * owq_gated_plan -- the launch shape of a gated product over two N x K layers, M tokens, on a device
+ * with `sms` SMs (host only; no device, no handle).
+ *   OWQ_GATED_FORWARD     the product of owq_gated_gemm, owq_gated_grad and owq_gated_backward's first
+ *                         part: tiles of 128 output rows x tile_tokens, K / 128 steps
+ *   OWQ_GATED_INPUT_GRAD  owq_gated_input_grad: tiles of 256 columns x tile_tokens, 2 ceil(N / 128) steps
+ *   OWQ_GATED_BACKWARD    the same as owq_gated_backward's second part (up to 32 tokens: two rows a token)
+ * A tile takes a pair of SMs.  The first `whole` tiles are computed at once, each of the others in
+ * `splits` parts of `steps` steps (the last one what is left), added in order by a reduction.
+ * Out: plan[0] tile_tokens (64, 128, 192 or 256), plan[1] tiles, plan[2] whole, plan[3] splits (1: whole
+ *      == tiles), plan[4] steps of a part.
+ * Errors: OWQ_ERR_NULL (plan NULL), OWQ_ERR_SHAPE (N, K outside owq_pack's ranges, M outside 1..65536),
+ * OWQ_ERR_ARG (sms < 1, unknown product).
+ */
+#define OWQ_GATED_FORWARD     0
+#define OWQ_GATED_INPUT_GRAD  1
+#define OWQ_GATED_BACKWARD    2
+owq_status_t owq_gated_plan(int N, int K, int M, int sms, int product, int plan[5]);
+
+/*
  * owq_gated_gemm -- h for any M (1..65536) on the 5th-generation tensor cores (tuned for
  * M >= 64).  ws: device workspace of ws_bytes (OWQ_ERR_NOMEM if it is too small).
  */

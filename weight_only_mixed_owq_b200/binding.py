@@ -25,6 +25,7 @@ STATUS_NAMES = {
 }
 OWQ_ACT_SILU, OWQ_ACT_GELU, OWQ_ACT_GELU_TANH = 0, 1, 2
 OWQ_F32, OWQ_F16, OWQ_BF16 = 0, 1, 2
+OWQ_GATED_FORWARD, OWQ_GATED_INPUT_GRAD, OWQ_GATED_BACKWARD = 0, 1, 2
 OWQ_INJECT_NONE, OWQ_INJECT_GEMV_TAG, OWQ_INJECT_GEMM_ARRIVE, OWQ_INJECT_BOUNDS = 0, 1, 2, 3
 OWQ_INJECT_CLIP, OWQ_INJECT_GATED = 4, 5
 
@@ -49,6 +50,7 @@ PROTOTYPES = [
     ("owq_input_grad", _I, [_P, _P, _P, _I, _P]),
     ("owq_gated_gemv", _I, [_P, _P, _I, _P, _P, _I, _P]),
     ("owq_gated_workspace", _I, [_P, _P, _I, _SZ]),
+    ("owq_gated_plan", _I, [_I, _I, _I, _I, _I, ctypes.POINTER(_I)]),
     ("owq_gated_gemm", _I, [_P, _P, _I, _P, _P, _I, _P, ctypes.c_size_t, _P]),
     ("owq_gated_grad", _I, [_P, _P, _I, _P, _P, _P, _P, _I, _P, ctypes.c_size_t, _P]),
     ("owq_gated_backward", _I, [_P, _P, _I, _P, _P, _P, _P, _P, _I, _P, ctypes.c_size_t, _P]),
@@ -212,6 +214,13 @@ def owq_gated_workspace(gate, up, M):
     n = ctypes.c_size_t()
     st = LIB.owq_gated_workspace(gate, up, M, ctypes.byref(n))
     return st, n.value
+
+
+def owq_gated_plan(N, K, M, sms, product):
+    """Returns (status, {tile_tokens, tiles, whole, splits, steps}): a gated product's launch shape."""
+    out = (ctypes.c_int * 5)()
+    st = LIB.owq_gated_plan(N, K, M, sms, product, out)
+    return st, dict(zip(("tile_tokens", "tiles", "whole", "splits", "steps"), out))
 
 
 def owq_gated_gemm(gate, up, act, x, h, M, ws, ws_bytes, stream=None) -> int:

@@ -601,6 +601,20 @@ owq_status_t owq_gated_workspace(owq_layer_t gate, owq_layer_t up, int M, size_t
   return OWQ_OK;
 }
 
+owq_status_t owq_gated_plan(int N, int K, int M, int sms, int product, int plan[5]) {
+  if (!plan) return OWQ_ERR_NULL;
+  if (N < 1 || N > (1 << 20) || K < kBlockCodes || K > 65536 || K % kBlockCodes || M < 1 || M > 65536)
+    return OWQ_ERR_SHAPE;
+  if (sms < 1 || product < OWQ_GATED_FORWARD || product > OWQ_GATED_BACKWARD) return OWQ_ERR_ARG;
+  const GatedPlan g = gated_plan(N, K, M, sms, product);
+  plan[0] = g.tile_tokens;
+  plan[1] = g.tiles;
+  plan[2] = g.whole;
+  plan[3] = g.splits;
+  plan[4] = g.steps;
+  return OWQ_OK;
+}
+
 owq_status_t owq_gated_gemm(owq_layer_t gate, owq_layer_t up, int act, const uint16_t* x, uint16_t* h, int M, void* ws,
                             size_t ws_bytes, owq_stream_t stream) {
   Layer *g, *u;

@@ -1032,6 +1032,13 @@ int pick_tile(int M, long long rows, int steps, int sms, TileCost (*cost)(int), 
   }
   return best;
 }
+// the tiles of the forward product (128 output rows a pair) and of the input gradient (256 columns a pair)
+int fwd_tiles(int N, int K, int M, int sms, TileSplit& split) {
+  return pick_tile(M, (N + 2 * kHalfRows - 1) / (2 * kHalfRows), K / kStepCodes, sms, fwd_cost, split);
+}
+int ig_tiles(int N, int K, int M, int sms, TileSplit& split) {
+  return pick_tile(M, (K / kStepCodes + 1) / 2, 2 * ((N + 127) / 128), sms, ig_cost, split);
+}
 size_t partial_bytes(const TileSplit& s, int BN) {
   return s.splits > 1 ? up256((size_t)s.splits * (s.tiles - s.whole) * 2 * BN * kBM * sizeof(float)) : 0;
 }
@@ -1061,7 +1068,7 @@ struct FwdPlan {
 FwdPlan fwd_plan(const Layer& gate, const Layer& up, int M) {
   FwdPlan f;
   f.rts = (gate.N + 2 * kHalfRows - 1) / (2 * kHalfRows);
-  f.BN = pick_tile(M, f.rts, gate.K / kStepCodes, layer_sm_count(gate.device), fwd_cost, f.split);
+  f.BN = fwd_tiles(gate.N, gate.K, M, layer_sm_count(gate.device), f.split);
   size_t at = 0;
   const Layer* L[2] = {&gate, &up};
   for (int l = 0; l < 2; ++l) {
@@ -1171,7 +1178,7 @@ IgPlan ig_plan(const Layer& gate, const Layer& up, int tokens, bool halves = fal
   const int M = halves ? 2 * tokens : tokens;
   f.halves = halves;
   const int sms = layer_sm_count(gate.device);
-  f.BN = pick_tile(M, (gate.K / kStepCodes + 1) / 2, 2 * ((gate.N + 127) / 128), sms, ig_cost, f.split);
+  f.BN = ig_tiles(gate.N, gate.K, M, sms, f.split);
   f.ldy = (gate.N + 7) & ~7;
   size_t at = 0;
   for (int l = 0; l < 2; ++l) {
@@ -1329,6 +1336,13 @@ BwdPlan bwd_plan(const Layer& gate, const Layer& up, int M) {
   return b;
 }
 }  // namespace
+GatedPlan gated_plan(int N, int K, int M, int sms, int product) {
+  TileSplit s;
+  const int BN = product == OWQ_GATED_FORWARD
+                     ? fwd_tiles(N, K, M, sms, s)
+                     : ig_tiles(N, K, product == OWQ_GATED_BACKWARD && M <= kHalvesM ? 2 * M : M, sms, s);
+  return {BN, s.tiles, s.whole, s.splits, s.steps};
+}
 size_t gated_backward_ws_bytes(const Layer& gate, const Layer& up, int M) { return bwd_plan(gate, up, M).total; }
 owq_status_t gated_backward_sm100(const Layer& gate, const Layer& up, int act, const __half* x, const __half* dh, __half* dg,
                                   __half* du, __half* dx, int M, void* ws, size_t ws_bytes, long long wait_limit,
@@ -1348,7 +1362,6 @@ owq_status_t gated_backward_sm100(const Layer& gate, const Layer& up, int act, c
                         : dispatch_ig<4>(gate, up, dy[0], dy[1], dx, M, b.g, w, wait_limit, skip_arrive, s);
 }
 
-size_t gated_gemm_ws_bytes(const Layer& gate, const Layer& up, int M) { return fwd_plan(gate, up, M).total; }
 size_t gated_input_grad_ws_bytes(const Layer& gate, const Layer& up, int M) { return ig_plan(gate, up, M).total; }
 
 owq_status_t gated_gemm_sm100(const Layer& gate, const Layer& up, int act, const __half* x, const __half* dh, __half* out0,

@@ -194,8 +194,7 @@ bool encode_gated_maps(Layer& L);
 cudaError_t launch_gated_gemv(const Layer& gate, const Layer& up, int act, const __half* x, __half* h, int M,
                               long long wait_limit, bool skip, cudaStream_t s);
 // many tokens: h = act(g) u (dh NULL, out0 = h), or the gradients of both projections' outputs
-// (out0 = dg, out1 = du); ws: the caller's workspace of at least gated_gemm_ws_bytes
-size_t gated_gemm_ws_bytes(const Layer& gate, const Layer& up, int M);
+// (out0 = dg, out1 = du); ws: the caller's workspace
 owq_status_t gated_gemm_sm100(const Layer& gate, const Layer& up, int act, const __half* x, const __half* dh, __half* out0,
                               __half* out1, int M, void* ws, size_t ws_bytes, long long wait_limit, bool skip_arrive,
                               cudaStream_t s);
@@ -208,6 +207,11 @@ size_t gated_backward_ws_bytes(const Layer& gate, const Layer& up, int M);
 owq_status_t gated_backward_sm100(const Layer& gate, const Layer& up, int act, const __half* x, const __half* dh, __half* dg,
                                   __half* du, __half* dx, int M, void* ws, size_t ws_bytes, long long wait_limit,
                                   bool skip_arrive, cudaStream_t s);
+// launch shape of one of their products (OWQ_GATED_*)
+struct GatedPlan {
+  int tile_tokens, tiles, whole, splits, steps;
+};
+GatedPlan gated_plan(int N, int K, int M, int sms, int product);
 // SM count of device `dev` (cached per device ordinal)
 int layer_sm_count(int dev);
 // Raise a kernel's dynamic shared memory limit, once per device (a bit of `done` each; the caller
