@@ -556,7 +556,13 @@ class OwqGated:
 class OwqGradClip:
     """The gradient tensors that a step clips together (see owq_clip_create in include/owq.h):
     fp32, fp16 or bf16, contiguous, on one device.  `outs` takes the clipped values (None: in
-    place).  Calling it with max_norm returns the global norm, a device tensor of one fp32."""
+    place).  Calling it with max_norm returns the global norm, a device tensor of one fp32.
+
+    The list holds the tensors' addresses: a step refills the same tensors (weak_grad(..., dw=t));
+    gradients that are made anew each step want clip_grads, which makes a list for one call.  Calls
+    of one list must be ordered (one stream, or synchronised).  A norm that is not finite clips
+    nothing: the caller reads it and skips the step (torch's clip_grad_norm_ would write zeros or
+    NaN)."""
 
     def __init__(self, grads, outs=None, stream=None):
         import torch
