@@ -486,6 +486,36 @@ k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {
   cluster_sync();   // no CTA leaves while its sums may still be read
 }
 
+// Clusters of `cl` CTAs that run at once, one CTA per SM (0: the driver did not say).  Fewer than SMs / cl
+// from 4 CTAs on, as a cluster stays within a GPC: a grid of SMs / cl clusters would leave some for a second
+// wave as long as the first (16384 x 8192, 4-bit, 12 tokens: 100 us with 37 clusters of 4).  Asked once per
+// device and size.
+int resident_clusters(const void* kern, int cl, int sms, int dev) {
+  if (cl == 1) return sms;
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> known[kMaxDev][4];   // [log2 cl]
+  const int lg = cl == 2 ? 1 : cl == 4 ? 2 : 3;
+  int n = dev < kMaxDev ? known[dev][lg].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms / cl * cl);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kMaxSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cl;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (dev < kMaxDev) known[dev][lg].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // Items and rings that fit beside the activations, the largest items first (an item costs a warp
 // about 70 instructions beside the 300 of each unit; one stage in flight per warp covers the
 // latency of the loads from about 40 KB an SM); then the same with K split over 2, 4 and 8 CTAs;
@@ -495,14 +525,17 @@ template <int BITS, int NT, bool PG>
 cudaError_t launch_p(GatedGemvArgs& a, int all, int sms, int dev, cudaStream_t s) {
   static std::atomic<unsigned long long> allowed[2];   // [activations in shared memory]
   static constexpr int kShapes[][2] = {{4, 2}, {3, 2}, {2, 2}, {1, 3}};
-  int pieces = 0, smem = 0, xs = 0, per = 0;
+  int pieces = 0, smem = 0, xs = 0, per = 0, resident = 0;
+  const void* clustered = (const void*)k_gated_gemv<BITS, NT, PG, true>;
   auto fits = [&](int cl, int n, int x) {
     a.cl = cl;
     per = (all + n - 1) / n;
-    const int clusters = std::max(1, std::min(per, sms / cl));
+    if (a.K / kBlockCodes < cl) return false;
+    if (cl > 1 && allow_smem(clustered, kMaxSmem, dev, allowed[1]) != cudaSuccess) return false;
+    if ((resident = resident_clusters(clustered, cl, sms, dev)) < 1) return false;
+    const int clusters = std::max(1, std::min(per, resident));
     a.tcap = (per + clusters - 1) / clusters;
     a.bcap = (a.K / kBlockCodes + cl - 1) / cl;
-    if (a.K / kBlockCodes < cl) return false;
     for (const auto& sh : kShapes) {
       a.sub = sh[0];
       a.stages = sh[1];
@@ -524,7 +557,7 @@ cudaError_t launch_p(GatedGemvArgs& a, int all, int sms, int dev, cudaStream_t s
   if (e != cudaSuccess) return e;
   for (a.log_cl = 0; 1 << a.log_cl < a.cl;) ++a.log_cl;
   for (a.tile0 = 0; a.tile0 < all; a.tile0 += per) {
-    const int tiles = std::min(per, all - a.tile0), clusters = std::max(1, std::min(tiles, sms / a.cl));
+    const int tiles = std::min(per, all - a.tile0), clusters = std::max(1, std::min(tiles, resident));
     a.base = tiles / clusters;
     a.extra = tiles % clusters;
     cudaLaunchConfig_t cfg = {};
