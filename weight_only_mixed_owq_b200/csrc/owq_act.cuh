@@ -5,9 +5,10 @@
 //              a' = s + 2 g s (1 - s) v'
 // The erfc and logistic forms keep the relative accuracy of the small values at large negative
 // g, where 1 + erf and 1 + tanh cancel; e^x overflowing to infinity gives s = 0, as it should.
-// The logistic uses the hardware's exponential and reciprocal (relative errors of about
-// 2^-22 + |x| 2^-24 and 2^-23: far inside the outputs' fp16 rounding of 2^-11); with the
-// correctly rounded ones the epilogue of a 256-token tile took 3 us more.
+// The logistic uses __expf and __fdividef: documented to within 2 + floor(1.173 |x|) and 2 units in the
+// last place (2^-23 relative), so that s is off by at most (4 + 1.173 |x|) 2^-23 of itself, 2^-16 where
+// e^x leaves fp32's range (and 0 below 2^-126): far inside the outputs' fp16 rounding of 2^-11.
+// With expf and a division the epilogue of a 256-token tile took 3 us more.
 #pragma once
 #include <type_traits>
 

@@ -13,8 +13,8 @@
 // are read.
 // Measured: 202 MB of fp32 in 224 tensors 97 us; 333 MB read, so that 71 MB of the second pass's
 // input came from the ring and L2: 535 MB through memory, 5.5 TB/s.
-// Squares are added in fp64, eight values' worth at a time: those are summed in fp32 (2^-24 each,
-// averaging out) where that neither overflows nor loses small values, else one by one in fp64 (a
+// Squares are added in fp64, 16 bytes of values at a time (4 of fp32, 8 of fp16 or bf16): those are summed in
+// fp32 (2^-24 each, averaging out) where that neither overflows nor loses small values, else one by one in fp64 (a
 // conversion per value would take as long as the memory).  All sums run in a fixed order: repeated
 // calls give identical bits.
 #include <cuda_bf16.h>

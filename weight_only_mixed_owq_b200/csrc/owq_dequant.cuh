@@ -1,5 +1,5 @@
-// Bit-exact dequantisation of code pairs in registers, for the gated block's kernels: a pair of
-// neighbouring codes of a row -> fp16x2 W_hat = fp16_rn(s (q - z)).
+// fp16x2 arithmetic, and the bit-exact dequantisation of code pairs in registers that the gated block's
+// kernels use: a pair of neighbouring codes of a row -> fp16x2 W_hat = fp16_rn(s (q - z)).
 //
 // The pair is lifted as (bits | 0x6400) per half, the fp16 value 1024 + q 2^o (o: the code's bit
 // offset); times 2^-o plus -(1024 2^-o + z) is q - z exactly (one fma.rn.f16x2), and the product
@@ -11,17 +11,18 @@
 namespace owq {
 namespace {
 
-__device__ __forceinline__ uint32_t dq_fma(uint32_t a, uint32_t b, uint32_t c) {
+// fp16x2 helpers (exact integer arithmetic on small values)
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
-__device__ __forceinline__ uint32_t dq_mul(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ uint32_t dq_sub(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
@@ -79,7 +80,7 @@ struct RowDq {
     const uint32_t z2 = __byte_perm(sz, sz, 0x3232);
     #pragma unroll
     for (int c = 0; c < kNC; ++c)   // -2^(10 - o) as fp16, both halves
-      nz[c] = dq_sub((0x8000u | ((uint32_t)(25 - class_off<BITS>(c)) << 10)) * 0x00010001u, z2);
+      nz[c] = h2_sub((0x8000u | ((uint32_t)(25 - class_off<BITS>(c)) << 10)) * 0x00010001u, z2);
   }
 };
 
@@ -87,7 +88,7 @@ template <int BITS>
 __device__ __forceinline__ uint32_t dequant(const uint32_t* w, int j, const RowDq<BITS>& dq) {
   const int c = pair_class<BITS>(j);
   const uint32_t scl = ((uint32_t)(15 - class_off<BITS>(c)) << 10) * 0x00010001u;   // 2^-o
-  return dq_mul(dq_fma(pair_lifted<BITS>(w, j), scl, dq.nz[c]), dq.s2);
+  return h2_mul(h2_fma(pair_lifted<BITS>(w, j), scl, dq.nz[c]), dq.s2);
 }
 
 }  // namespace

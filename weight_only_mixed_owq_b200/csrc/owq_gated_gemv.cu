@@ -96,12 +96,6 @@ inline int smem_plan(GatedGemvArgs& a, int stage, int MT, bool pg, bool xsmem) {
   return a.o_x + std::max(rows, sums);
 }
 
-__device__ __forceinline__ uint32_t lds_u1(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-
 template <int BITS, int NT, bool PG, bool XSMEM>
 __global__ void __launch_bounds__(kThreads, 1)
 k_gated_gemv(const __grid_constant__ GatedGemvArgs a) {

@@ -1,7 +1,7 @@
 // What the tcgen05 products share: the tile geometry, the bit-exact fp16x2 dequantisation of a
 // code pair, and the tensor maps of the packed layout.
 #pragma once
-#include "owq_format.cuh"
+#include "owq_dequant.cuh"
 #include "owq_internal.cuh"
 #include "owq_sm100.cuh"
 
@@ -26,22 +26,6 @@ struct Smem {
 template <int BITS, int BN, int S>
 constexpr int smem_bytes() { return S * Smem<BITS, BN>::kStage + 1024 /*barriers*/ + 1024 /*align slack*/; }
 
-// fp16x2 helpers (exact integer arithmetic on small values)
-__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 __device__ __forceinline__ uint32_t h2_splat(float v) {
   __half h = __float2half_rn(v);
   uint32_t u = __half_as_ushort(h);
