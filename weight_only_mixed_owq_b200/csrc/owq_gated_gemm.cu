@@ -11,9 +11,9 @@
 // type that activations and gradients have at every layer boundary of this library), dx once.
 //
 // Bound: the tensor cores from about 200 tokens (4 M N K flops forward, 8 M N K backward), the
-// packed weights' bytes below.  Measured (GPU time): 13824 x 5120, 3-bit, 2048 tokens forward 391 us
-// (1.48 PFLOP/s), backward 843 us (1.38); 11008 x 4096, 4-bit, 64 tokens forward 27.6 us, 256 tokens
-// backward 94 us.  Below 256 tokens a step (128 codes of 256 MMA rows by the tile's tokens) is paced
+// packed weights' bytes below.  Measured (GPU time in short graphs; in brackets called back to back for a
+// second, power-capped): 13824 x 5120, 3-bit, 2048 tokens forward 393 (457) us, 1.48 (1.27) PFLOP/s, backward
+// 850 (1008) us; 11008 x 4096, 4-bit, 64 tokens forward 27.6 (30.6) us, 256 tokens backward 96 (111) us.  Below 256 tokens a step (128 codes of 256 MMA rows by the tile's tokens) is paced
 // by forming the A operand: 0.35 / 0.39 / 0.50 us at 64 / 128 / 192 tokens (3-bit), 0.67 us at 256,
 // where the MMAs alone want 0.53 us at the full clock.
 #include <algorithm>

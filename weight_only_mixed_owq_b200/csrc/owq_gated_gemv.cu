@@ -7,8 +7,8 @@
 // and the product of two projections doubles that).  Sums, activation and product are fp32; h
 // is rounded once.
 //
-// Bound: reading the packed weights once (HBM), closely followed by the issue of the unpack
-// (about 130 warp instructions per 16 x 128 codes).
+// Bound: reading the packed weights once (HBM), closely followed by the unpack (about 130 warp
+// instructions per 16 x 128 codes, four warps a scheduler).
 //
 // Split.  The unit is a pair tile (16 gate rows and the same 16 up rows) x one 128-code block.
 // A tensor-core fragment (m16n8k16) takes 8 gate rows as its rows 0-7 and the 8 up rows of the
@@ -33,9 +33,10 @@
 // distributed shared memory: repeated calls give identical bits.
 //
 // Measured (a graph of calls over three copies of the weights, GPU time per call): 11008 x 4096,
-// 4-bit, one token 13.9 us (49.4 MB, 3.5 TB/s; a further tile of 16 x 4096 per CTA costs 1.95 us,
+// 4-bit, one token 14.0 us (49.4 MB, 3.5 TB/s; a further tile of 16 x 4096 per CTA costs 1.95 us,
 // 5.4 TB/s, the rest about 5.7 us a launch); 13824 x 5120, 3-bit, 16 tokens 28.5 us (two token tiles
-// through the products: issue-bound, 2.2 warp instructions a cycle per SM).
+// through the products: 2.2 of 4 warp instructions a cycle per SM, tensor pipe 26%, DRAM 23%, so probably the
+// latency of unpack, fma, mul and MMA with four warps a scheduler).
 #include "owq_act.cuh"
 #include "owq_dequant.cuh"
 #include "owq_internal.cuh"
